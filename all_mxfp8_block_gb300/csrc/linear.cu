@@ -1,0 +1,578 @@
+// Grouped MXFP8 product with a fused epilogue (bias, activation, residual,
+// BF16 / FP32 / MXFP8 output), for sm_103a.
+//
+//   out[q][p] = act( sum_c Q[q][c] P[p][c] + bias[p] ) + residual[q][p]
+//
+// One orientation serves every use: the P rows (weight rows) are the MMA's 128
+// accumulator lanes, the Q rows (tokens) its columns, 32 to 256 of them.  A
+// decode step's few tokens then cost a 32-column tile, the weights stream
+// through once, and an output row is written by neighbouring lanes.
+//
+// CTA roles: warps 0 and 2 issue the TMA loads (even / odd stages), warp 1 owns
+// the tensor memory and issues the MMAs, warps 4-7 move the stages' scale bytes
+// into tensor memory (one warp per lane quarter), the warps from 8 on are the
+// epilogue.  A stage is one 128-wide block of the contraction: 128 P rows,
+// tile_q Q rows (128-byte swizzled) and their scale tiles.  CTAs are
+// persistent over tiles.  With few tiles a cluster of up to 8 CTAs shares a
+// tile's contraction: each accumulates its part, the partial tiles meet in
+// distributed shared memory and every CTA sums (in rank order) and finishes
+// its share of the columns, in the same launch.
+//
+// Segments start at multiples of 32 rows, so a token tile may start inside a
+// 128-row scale tile: the scale warps shift the columns while they copy.  A
+// contraction range may start and end inside a 128-wide block: the MMA's
+// 32-wide steps outside it are not issued.
+//
+// Every wait is bounded; after one ran out the CTA goes on without waiting (its
+// output is then undefined) and the status block tells.
+#include <algorithm>
+
+#include "linear.cuh"
+#include "mxquant.cuh"
+#include "ptx.cuh"
+
+namespace mxa2a {
+using namespace ptx;
+
+namespace {
+
+constexpr int kMaxGroups = 1024;
+constexpr int kLinMaxStages = 6;
+
+// 32 lanes x 16 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+template <int TQ>
+struct LinCfg {
+    static constexpr int kStages = TQ == 256 ? 4 : (TQ == 128 ? 6 : 4);
+    static constexpr int kCtasPerSm = TQ <= 64 ? 2 : 1;
+    static constexpr int kEpiWarps = TQ >= 128 ? 8 : 4;
+    static constexpr int kThreads = 256 + 32 * kEpiWarps;
+    static constexpr int kAccBufs = TQ == 256 ? 1 : 2;
+    static constexpr int kQAtoms = TQ == 32 ? 1 : TQ / 128 + (TQ == 64 ? 2 : 1);   // scale tiles a Q tile may touch
+    static constexpr int kQCols = TQ / 32 < 4 ? 4 : TQ / 32;                        // TMEM columns of its scales
+    static constexpr uint32_t kSfCol = TQ * kAccBufs;
+    static constexpr uint32_t kSfCols = 4 + kQCols;
+    static constexpr uint32_t kTmem = TQ <= 32 ? 128 : (TQ == 64 ? 256 : 512);
+    static constexpr int kQBytes = TQ * 128;
+    static constexpr int kColsPerWarp = TQ / (kEpiWarps / 4);
+    static constexpr size_t oP = 0;
+    static constexpr size_t oQ = oP + (size_t)kStages * kAStageBytes;
+    static constexpr size_t oSfp = oQ + (size_t)kStages * kQBytes;
+    static constexpr size_t oSfq = oSfp + (size_t)kStages * 512;
+    static constexpr size_t oCtl = oSfq + (size_t)kStages * kQAtoms * 512;
+    static constexpr size_t ctl_bytes();
+    static_assert(kSfCol + kStages * kSfCols <= kTmem, "tensor memory columns");
+    // a split tile's fp32 partial [TQ][128] lies over the P stages, which its MMAs have read
+    static_assert(TQ * 512 <= kStages * (kAStageBytes + kQBytes), "partial tile");
+};
+
+struct __align__(8) LinCtl {
+    uint64_t full[kLinMaxStages], empty[kLinMaxStages], sf_full[kLinMaxStages], sf_ready[kLinMaxStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    volatile int abort;
+    volatile int issued[2];           // stages issued by each producer
+    int total;                        // tiles of all groups
+    int start[kMaxGroups + 1];        // first tile of each group (grouped Q rows)
+};
+template <int TQ>
+constexpr size_t LinCfg<TQ>::ctl_bytes() { return oCtl + sizeof(LinCtl) + 1024; }
+
+__device__ __noinline__ void lin_report(const LinParams& p, int role, long long parity) {
+    DevStatus* st = p.status;
+    const unsigned long long mine = (p.launch_id << 8) | (unsigned long long)kErrTimeout;
+    unsigned long long cur = atomicAdd(&st->key, 0ull);
+    for (;;) {
+        if ((cur >> 8) == p.launch_id) return;   // this launch already reported
+        const unsigned long long prev = atomicCAS(&st->key, cur, mine);
+        if (prev == cur) break;
+        cur = prev;
+    }
+    st->role = role;
+    st->block = blockIdx.x;
+    st->step = st->segment = st->slot = -1;
+    st->observed = -1;
+    st->expected = parity;
+    __threadfence();
+}
+
+// Bounded wait for an mbarrier phase.  After a time-out anywhere in the CTA
+// every later wait returns at once, so that all roles reach the end together.
+__device__ __forceinline__ void lin_wait(const LinParams& p, LinCtl* ctl, uint64_t* bar, uint32_t parity, int role) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (ctl->abort) return;
+        if ((n & 63) == 0 && globaltimer() - t0 > (uint64_t)p.timeout_ns) {
+            lin_report(p, role, (long long)parity);
+            ctl->abort = 1;
+            return;
+        }
+    }
+}
+
+struct LinItem {
+    int group;
+    int p0;              // first P row inside the group
+    long long q0;        // first Q row
+    long long q_end;     // Q rows past this are not this tile's (segment end)
+    long long q_live;    // Q rows past this are padding: zeros are written
+    int b0, b1;          // 32-blocks of the contraction
+    int kb0, kb1;        // 128-blocks this CTA reads
+};
+
+__device__ __forceinline__ int seg_start(const LinParams& p, int g, long long limit) {
+    // 32-row granular and inside the buffers, whatever the array holds
+    const long long o = __ldg(p.offsets + g);
+    return (int)(max(0ll, min(o, limit)) & ~31ll);
+}
+
+template <int TQ>
+__device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ctl, int tile, int rank) {
+    LinItem it;
+    int p_tile, q_tile;
+    if (p.by_contraction) {
+        const int per = p.pt * p.qt;
+        it.group = tile / per;
+        const int r = tile - it.group * per;
+        q_tile = r / p.pt;
+        p_tile = r - q_tile * p.pt;
+        it.q0 = (long long)q_tile * TQ;
+        it.q_end = it.q_live = p.q_rows;
+        it.b0 = 0;
+        it.b1 = p.blocks;
+        if (p.offsets) {
+            it.b0 = seg_start(p, it.group, (long long)p.blocks * 32) / 32;
+            it.b1 = max(it.b0, seg_start(p, it.group + 1, (long long)p.blocks * 32) / 32);
+        }
+    } else {
+        int lo = 0, hi = p.groups - 1;   // the last group that starts at or before this tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (ctl->start[mid] <= tile) lo = mid; else hi = mid - 1;
+        }
+        it.group = lo;
+        const int first = ctl->start[lo], qt = (ctl->start[lo + 1] - first) / p.pt;
+        const int r = tile - first;
+        // bands of 16 P tiles, all Q tiles of a band before the next: the CTAs
+        // in flight share P and Q tiles in L2
+        const int band = r / (16 * qt), np = min(16, p.pt - band * 16), rb = r - band * 16 * qt;
+        q_tile = rb / np;
+        p_tile = band * 16 + rb - q_tile * np;
+        long long o = 0;
+        it.q_end = it.q_live = p.q_rows;
+        if (p.offsets) {
+            o = seg_start(p, lo, p.q_rows);
+            it.q_end = lo + 1 == p.groups ? min((long long)__ldg(p.offsets + lo + 1), (long long)p.q_rows)
+                                          : (long long)seg_start(p, lo + 1, p.q_rows);
+            it.q_live = min(it.q_end, o + max(0, __ldg(p.counts + lo)));
+        }
+        it.q0 = o + (long long)q_tile * TQ;
+        it.b0 = 0;
+        it.b1 = p.blocks;
+    }
+    it.p0 = p_tile * 128;
+    const int lo = it.b0 / 4, hi = it.b1 > it.b0 ? (it.b1 + 3) / 4 : lo;
+    const int per = (hi - lo + p.splits - 1) / p.splits;
+    it.kb0 = min(hi, lo + rank * per);
+    it.kb1 = min(hi, it.kb0 + per);
+    return it;
+}
+
+// ------------------------------------------------------------------ epilogue of NC columns
+// v[j]: the sums of this lane's feature (P row `f`) for tokens q + j.
+template <int NC>
+__device__ __forceinline__ void lin_store(const LinParams& p, const LinItem& it, int f, int lane, long long q, float (&v)[NC]) {
+    static_assert(NC % 4 == 0, "columns");
+    if (q >= it.q_end) return;   // (uniform over the warp)
+    const long long row0 = (p.by_contraction ? (long long)it.group * p.q_rows : 0) + q;
+    const bool odd = lane & 1;
+    const float b = p.bias ? __ldg(p.bias + (size_t)it.group * p.p_rows + f) : 0.f;
+    uint16_t* const pre = p.preact;
+    const int fe = f & ~1;       // the feature pair this lane stores
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] = q + j < it.q_live ? v[j] + b : 0.f;
+    if (pre) {
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+            const float got = __shfl_xor_sync(kLanes, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = odd ? bf16x2_bits(got, v[j + 1]) : bf16x2_bits(v[j], got);
+            if (q + j + odd < it.q_end) *reinterpret_cast<uint32_t*>(pre + (row0 + j + odd) * p.p_rows + fe) = w;
+        }
+    }
+    if (p.act != kActNone) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], p.act);   // (0 stays 0 on padding rows)
+    }
+    if (p.residual) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            if (q + j < it.q_live) v[j] += __uint_as_float((uint32_t)__ldg(p.residual + (row0 + j) * p.p_rows + f) << 16);
+    }
+    if (p.out_type == kTypeBf16) {
+        uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+            const float got = __shfl_xor_sync(kLanes, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = odd ? bf16x2_bits(got, v[j + 1]) : bf16x2_bits(v[j], got);
+            if (q + j + odd < it.q_end) *reinterpret_cast<uint32_t*>(out + (row0 + j + odd) * p.p_rows + fe) = w;
+        }
+    } else if (p.out_type == kTypeF32) {
+        float* out = static_cast<float*>(p.out);
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            if (q + j < it.q_end) out[(row0 + j) * p.p_rows + f] = v[j];
+    } else {
+        // the warp's 32 features are one MX block of every token
+        uint8_t* out = static_cast<uint8_t*>(p.out);
+        const bool e5m2 = p.out_type == kTypeE5M2;
+        const int emax = mx_emax(e5m2), kb = f >> 7;
+#pragma unroll
+        for (int j = 0; j < NC; j += 4) {
+            float s[4];
+            uint32_t bytes = 0, nan = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t byte = mx_scale_byte(__reduce_max_sync(kLanes, __float_as_uint(v[j + i]) & 0x7fffffffu), emax);
+                s[i] = v[j + i] * mx_inv_scale(byte);
+                if (byte == 255) nan |= 0x7fu << (8 * i);
+                bytes |= byte << (8 * i);
+            }
+            uint32_t w = fp8x2(s[0], s[1], e5m2) | fp8x2(s[2], s[3], e5m2) << 16;
+            // (a NaN block's codes are all NaN)
+            w = (w & ~((nan >> 6 & 0x01010101u) * 0xffu)) | nan;
+            // 4 x 4 byte transpose over four lanes: lane 4 a + i then holds features 4 a .. 4 a + 3 of token j + i
+            const uint32_t o1 = __shfl_xor_sync(kLanes, w, 1);
+            w = odd ? __byte_perm(o1, w, 0x7351) : __byte_perm(w, o1, 0x6240);
+            const uint32_t o2 = __shfl_xor_sync(kLanes, w, 2);
+            w = (lane & 2) ? __byte_perm(o2, w, 0x7632) : __byte_perm(w, o2, 0x5410);
+            const int i = lane & 3;
+            if (q + j + i < it.q_end) {
+                *reinterpret_cast<uint32_t*>(out + (row0 + j + i) * p.p_rows + (f & ~3)) = w;
+                if (lane < 4)
+                    p.out_scale[scale_word(kb, row0 + j + i, p.q_row_tiles) + ((f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i));
+            }
+        }
+    }
+}
+
+template <int TQ>
+__global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
+    linear_kernel(const __grid_constant__ LinParams p, const __grid_constant__ CUtensorMap map_p,
+                  const __grid_constant__ CUtensorMap map_q) {
+    using C = LinCfg<TQ>;
+    extern __shared__ uint8_t lin_smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem_raw) + 1023) & ~uintptr_t(1023));
+    LinCtl* ctl = reinterpret_cast<LinCtl*>(smem + C::oCtl);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
+    const int first = (int)blockIdx.x / p.splits, stride = (int)gridDim.x / p.splits;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+            mbar_init(&ctl->sf_full[s], 1);
+            mbar_init(&ctl->sf_ready[s], 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl->acc_full[b], 1);
+            mbar_init(&ctl->acc_empty[b], C::kEpiWarps);
+        }
+        ctl->abort = 0;
+        ctl->issued[0] = ctl->issued[1] = 0;
+        fence_mbarrier_init();
+        prefetch_tensormap(&map_p);
+        prefetch_tensormap(&map_q);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem, C::kTmem);
+        tmem_relinquish();
+    }
+    if (warp == 3) {
+        // first tile of every group
+        if (p.by_contraction) {
+            if (lane == 0) ctl->total = p.groups * p.pt * p.qt;
+        } else {
+            int carry = 0;
+            for (int g0 = 0; g0 < p.groups; g0 += 32) {
+                const int g = g0 + lane;
+                int n = 0;
+                if (g < p.groups) {
+                    long long len = p.q_rows;
+                    if (p.offsets) {
+                        const int lo = seg_start(p, g, p.q_rows);
+                        const long long hi = min((long long)__ldg(p.offsets + g + 1), (long long)p.q_rows);
+                        len = max(0ll, hi - lo);
+                    }
+                    n = (int)((len + TQ - 1) / TQ) * p.pt;
+                }
+                int inc = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int v = __shfl_up_sync(kLanes, inc, d);
+                    if (lane >= d) inc += v;
+                }
+                if (g < p.groups) ctl->start[g] = carry + inc - n;
+                carry += __shfl_sync(kLanes, inc, 31);
+            }
+            if (lane == 0) {
+                ctl->start[p.groups] = carry;
+                ctl->total = carry;
+            }
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem;
+    const int total = ctl->total;
+    const bool split = p.splits > 1;
+
+    if (split) cluster_sync();   // every CTA of the cluster runs before any reads its shared memory
+
+    if (warp == 0 || warp == 2) {
+        // ---------------------------------------------------------- TMA producers
+        const int pid = warp / 2;
+        int n = 0;
+        for (int tile = first; tile < total; tile += stride) {
+            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const int qa = (int)(it.q0 >> 7);                                   // first scale tile of the Q rows
+            const int atoms = min((int)((it.q0 & 127) + TQ + 127) >> 7, p.q_row_tiles - qa);
+            if (lane == 0) {
+                for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+                    if ((n & 1) != pid) continue;
+                    const int stage = n % C::kStages;
+                    lin_wait(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma);
+                    if (ctl->abort) break;
+                    mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
+                    bulk_load(smem + C::oSfp + stage * 512,
+                              p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
+                                  ((size_t)kb * p.pt + it.p0 / 128) * 512,
+                              512, &ctl->sf_full[stage]);
+                    bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512,
+                              p.q_scale + ((size_t)kb * p.q_row_tiles + qa) * 512, 512 * atoms, &ctl->sf_full[stage]);
+                    mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
+                    tma_load_2d(smem + C::oP + (size_t)stage * kAStageBytes, &map_p, &ctl->full[stage], kb * 128,
+                                (p.by_contraction ? 0 : it.group * p.p_rows) + it.p0);
+                    tma_load_2d(smem + C::oQ + (size_t)stage * C::kQBytes, &map_q, &ctl->full[stage], kb * 128, (int)it.q0);
+                    ctl->issued[pid] = n + 1;
+                }
+            }
+            __syncwarp();
+            if (split) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA issuer
+        const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | ((uint32_t)(TQ >> 3) << 17) |
+                                (1u << 23) | (8u << 24);
+        int n = 0, acc = 0;
+        for (int tile = first; tile < total; tile += stride) {
+            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            if (lane == 0 && it.kb1 > it.kb0) {
+                const int buf = acc % C::kAccBufs;
+                lin_wait(p, ctl, &ctl->acc_empty[buf], ((acc / C::kAccBufs) & 1) ^ 1, kRoleMma);
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(buf * TQ);
+                uint32_t some = 0;
+                for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+                    const int stage = n % C::kStages;
+                    const uint32_t ph = (n / C::kStages) & 1;
+                    lin_wait(p, ctl, &ctl->full[stage], ph, kRoleMma);
+                    lin_wait(p, ctl, &ctl->sf_ready[stage], ph, kRoleMma);
+                    if (ctl->abort) break;
+                    tc_fence_after();
+                    const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
+                    const uint64_t ad = smem_desc(smem_u32(smem + C::oP + (size_t)stage * kAStageBytes), 16, 1024, kLayoutSw128);
+                    const uint64_t bd = smem_desc(smem_u32(smem + C::oQ + (size_t)stage * C::kQBytes), 16, 1024, kLayoutSw128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (kb * 4 + k < it.b0 || kb * 4 + k >= it.b1) continue;
+                        mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc0 | ((uint32_t)k << 4) | ((uint32_t)k << 29), sf,
+                                     sf + 4, some);
+                        some = 1;
+                    }
+                    tc_commit(&ctl->empty[stage]);
+                }
+                tc_commit(&ctl->acc_full[buf]);
+                ++acc;
+            }
+            __syncwarp();
+            if (split) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------------------------------------------------- scale warps
+        const int quarter = warp & 3;
+        int n = 0;
+        for (int tile = first; tile < total; tile += stride) {
+            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const int shift = (int)(it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
+            for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+                const int stage = n % C::kStages;
+                lin_wait(p, ctl, &ctl->sf_full[stage], (n / C::kStages) & 1, kRoleScale);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)stage * C::kSfCols;
+                tmem_st_32x32b_x4(t, reinterpret_cast<const uint4*>(smem + C::oSfp + stage * 512)[lane]);
+                const uint8_t* sq = smem + C::oSfq + (size_t)stage * C::kQAtoms * 512;
+                // words 4 a + shift .. of the tiles' concatenated columns
+                if (shift == 0) {
+#pragma unroll
+                    for (int a = 0; a < C::kQCols / 4; ++a)
+                        tmem_st_32x32b_x4(t + 4 + 4 * a, reinterpret_cast<const uint4*>(sq + a * 512)[lane]);
+                } else {
+                    uint4 x = reinterpret_cast<const uint4*>(sq)[lane];
+#pragma unroll
+                    for (int a = 0; a < C::kQCols / 4; ++a) {
+                        const uint4 y = a + 1 < C::kQAtoms ? reinterpret_cast<const uint4*>(sq + (a + 1) * 512)[lane] : x;
+                        tmem_st_32x32b_x4(t + 4 + 4 * a, shift == 1   ? make_uint4(x.y, x.z, x.w, y.x)
+                                                         : shift == 2 ? make_uint4(x.z, x.w, y.x, y.y)
+                                                                      : make_uint4(x.w, y.x, y.y, y.z));
+                        x = y;
+                    }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->sf_ready[stage]);
+            }
+            __syncwarp();
+            if (split) {
+                cluster_sync();
+                cluster_sync();
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------- epilogue
+        const int quarter = warp & 3, part = (warp - 8) >> 2;
+        float* partial = reinterpret_cast<float*>(smem);   // [TQ][128]: the split tiles' (over the stages)
+        int acc = 0;
+        for (int tile = first; tile < total; tile += stride) {
+            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const bool live = it.kb1 > it.kb0;
+            const int buf = acc % C::kAccBufs;
+            const int f = it.p0 + quarter * 32 + lane;
+            const bool in_p = it.p0 + quarter * 32 < p.p_rows;   // (P rows come in blocks of 32: uniform over the warp)
+            const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * TQ + part * C::kColsPerWarp);
+            if (live) {
+                lin_wait(p, ctl, &ctl->acc_full[buf], (acc / C::kAccBufs) & 1, kRoleEpi);
+                __syncwarp();
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < C::kColsPerWarp; c += 16) {
+                float v[16];
+                if (live) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(t + (uint32_t)c, r);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                }
+                if (split) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) partial[(part * C::kColsPerWarp + c + j) * 128 + quarter * 32 + lane] = v[j];
+                } else if (in_p) {
+                    lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, v);
+                }
+            }
+            if (live) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
+                ++acc;
+            }
+            if (split) {
+                __syncwarp();
+                cluster_sync();
+                // this CTA's share of the columns, 4 at a time over the epilogue's column parts
+                const int share = TQ / p.splits, parts = C::kEpiWarps / 4;
+                for (int c = rank * share + part * 4; in_p && c < (rank + 1) * share; c += 4 * parts) {
+                    float v[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int s = 0; s < p.splits; ++s) {
+                        const uint32_t at = mapa_shared(smem_u32(partial + c * 128 + quarter * 32 + lane), s);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(ld_shared_cluster_u32(at + j * 512));
+                    }
+                    lin_store<4>(p, it, f, lane, it.q0 + c, v);
+                }
+                fence_proxy_async_shared();   // (this thread's writes, before TMA fills the stages again)
+                __syncwarp();
+                cluster_sync();   // the partial tiles have been read: the stages may be filled again
+            }
+        }
+    } else if (split) {
+        for (int tile = first; tile < total; tile += stride) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
+    __syncthreads();
+    if (ctl->abort && threadIdx.x == 0) {
+        // loads may still be in flight into this CTA's shared memory: give them
+        // time to land (bounded) before the CTA ends
+        const uint64_t t0 = globaltimer();
+        for (int s = 0; s < C::kStages; ++s) {
+            const int last = max(ctl->issued[0], ctl->issued[1]) - 1;
+            const int n = last - ((last - s) % C::kStages + C::kStages) % C::kStages;   // stage s's last use
+            if (n < 0) continue;
+            while (!(mbar_try_wait(&ctl->full[s], (n / C::kStages) & 1) && mbar_try_wait(&ctl->sf_full[s], (n / C::kStages) & 1)))
+                if (globaltimer() - t0 > (uint64_t)p.timeout_ns) break;
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+template <int TQ>
+cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas, cudaStream_t stream) {
+    using C = LinCfg<TQ>;
+    cudaError_t e = cudaFuncSetAttribute(linear_kernel<TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ctl_bytes());
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::ctl_bytes();
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)p.splits, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<TQ>, p, map_p, map_q);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas,
+                          cudaStream_t stream) {
+    switch (tile_q) {
+        case 32: return launch_tq<32>(p, map_p, map_q, ctas, stream);
+        case 64: return launch_tq<64>(p, map_p, map_q, ctas, stream);
+        case 128: return launch_tq<128>(p, map_p, map_q, ctas, stream);
+        default: return launch_tq<256>(p, map_p, map_q, ctas, stream);
+    }
+}
+
+int linear_ctas_per_sm(int tile_q) { return tile_q <= 64 ? 2 : 1; }
+
+}  // namespace mxa2a

@@ -1,0 +1,53 @@
+// Interface between the linear layer's C ABI (linear_api.cu) and its GEMM
+// kernel (linear.cu).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+
+namespace mxa2a {
+
+// One grouped block-scaled product
+//   out[q][p] = epilogue( sum_c Q[q][c] P[p][c] )
+// with P rows on the accumulator's lanes (128 to a tile) and Q rows on its
+// columns (tile_q to a tile).  In the layer's forward product and in its input
+// gradient P is the weights and Q the tokens; in its weight gradient P is the
+// transposed input and Q the transposed output gradient.
+struct LinParams {
+    int groups;
+    int by_contraction;        // 0: Q's rows are grouped, P has groups * p_rows rows;
+                               // 1: the contraction is grouped (its range is the segment), out has groups * q_rows rows
+    int p_rows, q_rows;        // rows of P per group; rows of Q
+    int blocks;                // 32-blocks along the contraction
+    int pt, qt;                // tiles of P per group; by_contraction: tiles of Q
+    int q_row_tiles;           // 128-row tiles of Q's scale array
+    int splits;                // CTAs of a cluster that share a tile's contraction (1, 2, 4, 8)
+    int fmt_p, fmt_q;          // MMA element codes: 0 E4M3, 1 E5M2
+    const int32_t *offsets, *counts;   // segments (null: one group of everything)
+    const uint8_t *p_scale, *q_scale;
+    size_t p_scale_group;      // bytes of one group's P scale tiles
+    // epilogue
+    const float* bias;         // [groups][p_rows] or null
+    int act;
+    const uint16_t* residual;  // bf16, laid out as out, or null
+    uint16_t* preact;          // bf16, laid out as out, or null
+    void* out;
+    int out_type;              // kTypeBf16, kTypeF32, kTypeE4M3, kTypeE5M2
+    uint8_t* out_scale;        // MX output: scale tiles
+    // bounded waits
+    DevStatus* status;
+    unsigned long long launch_id;
+    long long timeout_ns;
+};
+
+constexpr int kRoleScale = 7;
+
+// tile_q: 32, 64, 128 or 256.  ctas: CTAs to launch (a multiple of splits)
+cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas,
+                          cudaStream_t stream);
+// CTAs of the kernel that one SM holds at once
+int linear_ctas_per_sm(int tile_q);
+
+}  // namespace mxa2a

@@ -12,44 +12,13 @@
 
 #include "../../include/mxa2a.h"
 #include "kernels.cuh"
+#include "host.cuh"
 
 using namespace mxa2a;
 
 namespace {
 
 thread_local int g_last_error = MXA2A_OK;
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// 2D uint8 tensor [outer][inner] (inner contiguous), box [box_outer][128], 128-byte swizzle.
-bool encode_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {inner};
-    cuuint32_t box[2] = {(cuuint32_t)BK, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
 
 // C: bf16 [M][N] (N contiguous), box 32 rows x 32 columns, 64-byte swizzle
 // (the epilogue's TMA stores; see store_c_chunk).
@@ -95,6 +64,8 @@ int tile_span(int64_t M, int64_t cm, int64_t rows = BM) {
 }
 
 }  // namespace
+
+void mxa2a::set_last_error(int code) { g_last_error = code; }
 
 struct mxa2a_plan {
     int R;                  // K slices of the GEMM's A (1 for the all-gather)

@@ -1,0 +1,160 @@
+// Device helpers shared by the mixture-of-experts and linear-layer kernels:
+// typed loads as fp32, the MX scale of a 32-element block, E4M3 / E5M2
+// encoding, and the place of a scale byte in the MMA's scale tiles.
+//
+// MX block (OCP MX, as the library's input quantiser): the block's shared
+// exponent is X = floor(log2 amax) - emax (emax 8 for E4M3, 15 for E5M2),
+// clamped to >= -127; a code is the value / 2^X saturated to the format's
+// largest value and rounded to nearest even.  An all-zero block has scale
+// byte 0 and zero codes; a block holding an infinity or a NaN has scale 0xFF
+// (the E8M0 NaN) and NaN codes, so it cannot pass for numbers.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "kernels.cuh"
+
+namespace mxa2a {
+
+// element types (the C ABI's numbers)
+constexpr int kTypeBf16 = 0, kTypeF16 = 1, kTypeF32 = 2, kTypeE4M3 = 3, kTypeE5M2 = 4;
+constexpr uint32_t kLanes = 0xffffffffu;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// V consecutive elements of type T at p, as fp32 (V * sizeof(T) a multiple of
+// 16 and p aligned to 16 bytes, or V = 1)
+template <typename T, int V>
+struct Vec {
+    static_assert(V == 1 || (V * sizeof(T)) % 16 == 0, "vector width");
+    static constexpr int kWords = V * (int)sizeof(T) / 16;
+    __device__ static __forceinline__ void load(const T* p, float (&f)[V]) {
+        if constexpr (V == 1) {
+            f[0] = (float)*p;
+        } else {
+            uint4 w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            unpack(w, f);
+        }
+    }
+    __device__ static __forceinline__ void unpack(const uint4* w, float (&f)[V]) {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(u[i]);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                f[2 * i] = bf16_lo(u[i]);
+                f[2 * i + 1] = bf16_hi(u[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                f[2 * i] = t.x;
+                f[2 * i + 1] = t.y;
+            }
+        }
+    }
+    __device__ static __forceinline__ void store(T* p, const float (&f)[V]) {
+        if constexpr (V == 1) {
+            *p = (T)f[0];
+        } else {
+            uint32_t u[kWords * 4];
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[i] = __float_as_uint(f[i]);
+            } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) u[i] = bf16x2_bits(f[2 * i], f[2 * i + 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i) {
+                    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+                    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+        }
+    }
+};
+
+// scale byte of a block whose largest |value| has these fp32 bits (taken as an
+// unsigned maximum of the bit patterns, which orders NaN above infinity)
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, int emax) {
+    const int e = (int)(amax_bits >> 23);   // 0 for zero and for subnormals, which clamp to -127 as well
+    return e == 255 ? 255u : (uint32_t)max(e - emax, 0);
+}
+// 2^-X of a scale byte X + 127: always a normal number (X >= -127, X <= 119)
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// two codes, lo in the low byte (saturating, nearest even); nan: both NaN codes
+__device__ __forceinline__ uint32_t fp8x2(float lo, float hi, bool e5m2) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t mx_codes4(const float* v, float inv, bool bad, bool e5m2) {
+    if (bad) return 0x7f7f7f7fu;   // NaN in both formats
+    return fp8x2(v[0] * inv, v[1] * inv, e5m2) | fp8x2(v[2] * inv, v[3] * inv, e5m2) << 16;
+}
+__device__ __forceinline__ int mx_emax(bool e5m2) { return e5m2 ? 15 : 8; }
+
+// byte offset of the scale word (4 scales: 128 elements along the contraction)
+// of row r, contraction block kb of 128, among rt row tiles of 128 rows
+__device__ __forceinline__ size_t scale_word(int kb, long long r, int rt) {
+    return ((size_t)kb * rt + (size_t)(r >> 7)) * 512 + (size_t)((r & 31) * 16 + ((r & 127) >> 5) * 4);
+}
+
+// activations and their derivatives in fp32 (ids as in the C ABI).  tanh and
+// the logistic function through exp of a non-positive argument: no overflow,
+// and a relative error of a few fp32 roundings.
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
+// s = logistic(x), c = 1 - s, each to a few roundings of its own size
+__device__ __forceinline__ void logistic(float x, float& s, float& c) {
+    const float t = __expf(-fabsf(x));
+    const float h = __fdividef(1.f, 1.f + t), l = t * h;
+    s = x >= 0.f ? h : l;
+    c = x >= 0.f ? l : h;
+    if (x != x) s = c = x;
+}
+constexpr float kGeluA = 0.7978845608028654f, kGeluB = 0.044715f;   // sqrt(2 / pi)
+// 0.5 (1 + tanh u) = logistic(2 u)
+__device__ __forceinline__ float act_value(float z, int act) {
+    float s, c;
+    if (act == kActRelu) return z > 0.f || z != z ? z : 0.f;
+    if (act == kActGelu) {
+        logistic(2.f * kGeluA * (z + kGeluB * z * z * z), s, c);
+        return z * s;
+    }
+    if (act == kActSilu) {
+        logistic(z, s, c);
+        return z * s;
+    }
+    return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+    float s, c;
+    if (act == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    if (act == kActGelu || act == kActSilu) {
+        const bool g = act == kActGelu;
+        logistic(g ? 2.f * kGeluA * (z + kGeluB * z * z * z) : z, s, c);
+        const float t = s * c;
+        if (t == 0.f) return s;   // saturated: z's own size (it may be infinite) no longer matters
+        return s + z * t * (g ? 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z) : 1.f);
+    }
+    return 1.f;
+}
+
+}  // namespace mxa2a

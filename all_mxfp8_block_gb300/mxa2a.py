@@ -74,6 +74,17 @@ MXA2A_KIND_ALLGATHER = 1
 MXA2A_KIND_REDUCE_SCATTER = 2
 MXA2A_KIND_ALLREDUCE = 3
 
+MXA2A_TYPE_BF16 = 0
+MXA2A_TYPE_F16 = 1
+MXA2A_TYPE_F32 = 2
+MXA2A_TYPE_E4M3 = 3
+MXA2A_TYPE_E5M2 = 4
+
+MXA2A_ACT_NONE = 0
+MXA2A_ACT_RELU = 1
+MXA2A_ACT_GELU = 2
+MXA2A_ACT_SILU = 3
+
 MXA2A_WS_RING = 1
 MXA2A_WS_SFA = 2
 MXA2A_WS_SFB = 3
@@ -132,6 +143,28 @@ _SIGS = [
     ("mxa2a_l2_flush", ctypes.c_int, [_VP, ctypes.c_size_t, _VP]),
     ("mxa2a_run_noalloc", ctypes.c_int, [ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_int, _PP, _PP, _VP,
                                          _VP, _VP, _VP]),
+    ("mxa2a_moe_rows", _I64, [_I64, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("mxa2a_moe_sort", ctypes.c_int, [_I64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _I64, _VP, _VP, _VP, _VP, _VP,
+                                      _VP]),
+    ("mxa2a_moe_dispatch", ctypes.c_int, [_I64, ctypes.c_int, ctypes.c_int, _I64, _I64, _VP, ctypes.c_int, _I64, _VP,
+                                          _VP, _VP, _VP, ctypes.c_int, _VP, _VP]),
+    ("mxa2a_moe_combine", ctypes.c_int, [_I64, ctypes.c_int, _I64, _I64, _VP, ctypes.c_int, _VP, _VP, _VP, _VP, _VP]),
+    ("mxa2a_moe_combine_backward", ctypes.c_int, [_I64, ctypes.c_int, ctypes.c_int, _I64, _I64, _VP, ctypes.c_int, _VP,
+                                                  _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    ("mxa2a_scale_tiles_bytes", _I64, [_I64, _I64]),
+    ("mxa2a_scale_tiles", ctypes.c_int, [_VP, ctypes.c_int, _I64, _I64, _VP, _VP]),
+    ("mxa2a_quantize", ctypes.c_int, [_VP, ctypes.c_int, _I64, ctypes.c_int, _I64, _I64, ctypes.c_int, _VP, _VP, _VP,
+                                      _VP, _VP]),
+    ("mxa2a_linear_validate", ctypes.c_int, [ctypes.c_int, _I64, _I64, _I64]),
+    ("mxa2a_linear_create", _VP, [ctypes.c_int, _I64, _I64, _I64, ctypes.c_int]),
+    ("mxa2a_linear_run", ctypes.c_int, [_VP, _I64, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP, _VP,
+                                        ctypes.c_int, _VP, _VP, _VP]),
+    ("mxa2a_linear_backward", ctypes.c_int, [_VP, _I64, _VP, _VP, ctypes.c_int, ctypes.c_int, _VP, _VP, _VP, _VP, _VP,
+                                             _VP, ctypes.c_int, _VP, _VP, _VP, _VP]),
+    ("mxa2a_linear_get_status", ctypes.c_int, [_VP, ctypes.POINTER(mxa2a_status)]),
+    ("mxa2a_linear_set_option", ctypes.c_int, [_VP, ctypes.c_int, _I64]),
+    ("mxa2a_linear_get_option", ctypes.c_int, [_VP, ctypes.c_int, ctypes.POINTER(_I64)]),
+    ("mxa2a_linear_destroy", None, [_VP]),
     ("mxa2a_destroy", None, [_VP]),
     ("mxa2a_strerror", ctypes.c_char_p, [ctypes.c_int]),
 ]
@@ -358,6 +391,97 @@ def mxa2a_run_noalloc(R, M, kPerRank, N, commMSize, buffer_num, A_seg, A_scale_s
                                     _stream(stream)), "mxa2a_run_noalloc")
 
 
+# --- mixture-of-experts rows, MX quantisation, the linear layer ------------------
+def mxa2a_moe_rows(tokens, topk, experts, align) -> int:
+    return load().mxa2a_moe_rows(tokens, topk, experts, align)
+
+
+def mxa2a_moe_sort(tokens, topk, experts, align, rows, expert, offsets, counts, pos, src, stream=None) -> None:
+    _check(load().mxa2a_moe_sort(tokens, topk, experts, align, rows, _ptr(expert), _ptr(offsets), _ptr(counts),
+                                 _ptr(pos), _ptr(src), _stream(stream)), "mxa2a_moe_sort")
+
+
+def mxa2a_moe_dispatch(tokens, topk, experts, hidden, rows, x, x_type, ldx, pos, offsets, counts, out, out_type,
+                       out_scale=None, stream=None) -> None:
+    _check(load().mxa2a_moe_dispatch(tokens, topk, experts, hidden, rows, _ptr(x), x_type, ldx, _ptr(pos),
+                                     _ptr(offsets), _ptr(counts), _ptr(out), out_type, _ptr(out_scale),
+                                     _stream(stream)), "mxa2a_moe_dispatch")
+
+
+def mxa2a_moe_combine(tokens, topk, hidden, rows, y, type, pos, weight, residual, out, stream=None) -> None:
+    _check(load().mxa2a_moe_combine(tokens, topk, hidden, rows, _ptr(y), type, _ptr(pos), _ptr(weight),
+                                    _ptr(residual), _ptr(out), _stream(stream)), "mxa2a_moe_combine")
+
+
+def mxa2a_moe_combine_backward(tokens, topk, experts, hidden, rows, dout, type, y, pos, offsets, counts, weight, dy,
+                               dweight, stream=None) -> None:
+    _check(load().mxa2a_moe_combine_backward(tokens, topk, experts, hidden, rows, _ptr(dout), type, _ptr(y),
+                                             _ptr(pos), _ptr(offsets), _ptr(counts), _ptr(weight), _ptr(dy),
+                                             _ptr(dweight), _stream(stream)), "mxa2a_moe_combine_backward")
+
+
+def mxa2a_scale_tiles_bytes(rows, cols) -> int:
+    return load().mxa2a_scale_tiles_bytes(rows, cols)
+
+
+def mxa2a_scale_tiles(scale, groups, rows, cols, tiles, stream=None) -> None:
+    _check(load().mxa2a_scale_tiles(_ptr(scale), groups, rows, cols, _ptr(tiles), _stream(stream)),
+           "mxa2a_scale_tiles")
+
+
+def mxa2a_quantize(x, x_type, ldx, groups, rows, cols, format, codes, scale, codes_t=None, scale_t=None,
+                   stream=None) -> None:
+    _check(load().mxa2a_quantize(_ptr(x), x_type, ldx, groups, rows, cols, format, _ptr(codes), _ptr(scale),
+                                 _ptr(codes_t), _ptr(scale_t), _stream(stream)), "mxa2a_quantize")
+
+
+def mxa2a_linear_validate(groups, max_rows, N, K) -> int:
+    return load().mxa2a_linear_validate(groups, max_rows, N, K)
+
+
+def mxa2a_linear_create(groups, max_rows, N, K, training=0) -> int:
+    h = load().mxa2a_linear_create(groups, max_rows, N, K, int(training))
+    if not h:
+        raise Mxa2aError(load().mxa2a_last_error(), "mxa2a_linear_create")
+    return h
+
+
+def mxa2a_linear_run(layer, rows, x, x_scale, w, w_scale, out, out_type, out_scale=None, offsets=None, counts=None,
+                     bias=None, activation=MXA2A_ACT_NONE, residual=None, preact=None, stream=None) -> None:
+    _check(load().mxa2a_linear_run(layer, rows, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(out), out_type,
+                                   _ptr(out_scale), _ptr(offsets), _ptr(counts), _ptr(bias), activation,
+                                   _ptr(residual), _ptr(preact), _stream(stream)), "mxa2a_linear_run")
+
+
+def mxa2a_linear_backward(layer, rows, dy, preact, activation, grad_format, x_t, x_t_scale, w_t, w_t_scale, dx, dw,
+                          dw_type, dbias, offsets=None, counts=None, stream=None) -> None:
+    _check(load().mxa2a_linear_backward(layer, rows, _ptr(dy), _ptr(preact), activation, grad_format, _ptr(x_t),
+                                        _ptr(x_t_scale), _ptr(w_t), _ptr(w_t_scale), _ptr(dx), _ptr(dw), dw_type,
+                                        _ptr(dbias), _ptr(offsets), _ptr(counts), _stream(stream)),
+           "mxa2a_linear_backward")
+
+
+def mxa2a_linear_get_status(layer) -> dict:
+    st = mxa2a_status()
+    _check(load().mxa2a_linear_get_status(layer, ctypes.byref(st)), "mxa2a_linear_get_status")
+    return {f: getattr(st, f) for f, _ in mxa2a_status._fields_}
+
+
+def mxa2a_linear_set_option(layer, key: int, value: int) -> None:
+    _check(load().mxa2a_linear_set_option(layer, key, int(value)), f"mxa2a_linear_set_option({key})")
+
+
+def mxa2a_linear_get_option(layer, key: int) -> int:
+    v = ctypes.c_int64()
+    _check(load().mxa2a_linear_get_option(layer, key, ctypes.byref(v)), f"mxa2a_linear_get_option({key})")
+    return v.value
+
+
+def mxa2a_linear_destroy(layer) -> None:
+    if layer:
+        load().mxa2a_linear_destroy(layer)
+
+
 def mxa2a_destroy(plan) -> None:
     if plan:
         load().mxa2a_destroy(plan)
@@ -481,3 +605,47 @@ class AllReducePlan(Plan):
 
     def run_host(self, *a, **k):
         raise Mxa2aError(MXA2A_ERR_INVALID_OPTION, "an all-reduce plan has run and run_unfused only")
+
+
+class Linear:
+    """Owning wrapper of an ``mxa2a_linear*`` with the same calls as methods."""
+
+    def __init__(self, groups, max_rows, N, K, training=False):
+        self.groups, self.max_rows, self.N, self.K = groups, max_rows, N, K
+        self.handle = mxa2a_linear_create(groups, max_rows, N, K, training)
+
+    def run(self, rows, x, x_scale, w, w_scale, out, out_type, out_scale=None, offsets=None, counts=None, bias=None,
+            activation=MXA2A_ACT_NONE, residual=None, preact=None, stream=None):
+        mxa2a_linear_run(self.handle, rows, x, x_scale, w, w_scale, out, out_type, out_scale, offsets, counts, bias,
+                         activation, residual, preact, stream)
+
+    def backward(self, rows, dy, preact, activation, grad_format, x_t, x_t_scale, w_t, w_t_scale, dx, dw, dw_type,
+                 dbias, offsets=None, counts=None, stream=None):
+        mxa2a_linear_backward(self.handle, rows, dy, preact, activation, grad_format, x_t, x_t_scale, w_t, w_t_scale,
+                              dx, dw, dw_type, dbias, offsets, counts, stream)
+
+    def status(self) -> dict:
+        return mxa2a_linear_get_status(self.handle)
+
+    def set_option(self, key, value):
+        mxa2a_linear_set_option(self.handle, key, value)
+
+    def get_option(self, key) -> int:
+        return mxa2a_linear_get_option(self.handle, key)
+
+    def destroy(self):
+        if getattr(self, "handle", None):
+            mxa2a_linear_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.destroy()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass

@@ -512,6 +512,189 @@ int mxa2a_run_noalloc(int R, int64_t M, int64_t kPerRank, int64_t N, int64_t com
                       const void *const *A_seg, const void *const *A_scale_seg, const void *B, const void *B_scale,
                       void *C_bf16, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Mixture-of-experts rows and the linear layer: the operators on either side
+ * of an expert-parallel exchange.  A router's expert ids are sorted by expert,
+ * the tokens' rows go into that order (quantised to MXFP8 on the way where a
+ * block-scaled product reads them next), every expert multiplies its rows by
+ * its own weights, and the results come back in token order, weighted.
+ *
+ * Segments.  Expert e's rows are [offsets[e], offsets[e] + counts[e]) of the
+ * sorted row buffers; offsets[e + 1] - offsets[e] is counts[e] rounded up to
+ * the alignment, offsets[0] = 0 and offsets[experts] is the number of rows in
+ * use.  The rows of a segment past its last token are padding: the row
+ * operators write zeros there, and nothing reads or writes rows past
+ * offsets[experts].  `rows` is what the row buffers hold; nothing past it is
+ * touched whatever offsets, counts or pos hold.
+ *
+ * MXFP8 matrices.  A matrix X [rows][cols] is codes uint8 [rows][cols] (E4M3 or
+ * E5M2) and E8M0 scales, one per 32 elements along cols, in scale tiles: for
+ * every 128 columns and every 128 rows 512 bytes, [ceil(cols/128)][ceil(rows/128)][512],
+ * where row r's four scales of the 128 columns are the bytes from
+ * (r % 32) * 16 + (r % 128) / 32 * 4 on (the order in which the MMA reads them).
+ * mxa2a_scale_tiles makes them from plain [rows][cols/32] scales.  The shared
+ * exponent of a block is floor(log2(largest magnitude)) - 8 (E4M3) or - 15
+ * (E5M2), at least -127; codes are rounded to nearest even and saturate.  An
+ * all-zero block has scale byte 0; a block that holds an infinity or a NaN has
+ * scale 0xFF (NaN) and NaN codes.
+ *
+ * Except for the plan of a linear layer these calls keep no state and allocate
+ * nothing; they may be captured into a CUDA graph and run on any stream, each
+ * call's buffers being its own.  All are asynchronous on `stream` (a
+ * cudaStream_t, NULL = legacy default stream).  No output may overlap an input.
+ * Sums are taken in fp32 in a fixed order (the same bits every time) and
+ * rounded once to the output's type.
+ * Common errors: MXA2A_ERR_INVALID_SHAPE (a size rule broken),
+ * MXA2A_ERR_NULL_PTR (a required pointer missing), MXA2A_ERR_MISALIGNED,
+ * MXA2A_ERR_INVALID_OPTION (an unknown type or activation),
+ * MXA2A_ERR_UNSUPPORTED_DEVICE, MXA2A_ERR_CUDA (the launch failed).
+ * The pages have no counterpart of these operators. */
+
+/* Element types of rows and outputs. */
+enum mxa2a_type {
+    MXA2A_TYPE_BF16 = 0,
+    MXA2A_TYPE_F16 = 1,
+    MXA2A_TYPE_F32 = 2,
+    MXA2A_TYPE_E4M3 = 3,   /* MXFP8: E4M3 codes with scale tiles */
+    MXA2A_TYPE_E5M2 = 4    /* MXFP8: E5M2 codes with scale tiles */
+};
+
+/* Activations: max(z, 0); 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
+ * z / (1 + exp(-z)). */
+enum mxa2a_activation {
+    MXA2A_ACT_NONE = 0,
+    MXA2A_ACT_RELU = 1,
+    MXA2A_ACT_GELU = 2,
+    MXA2A_ACT_SILU = 3
+};
+
+/* Rows that hold any routing of tokens x topk assignments: tokens * topk +
+ * min(experts, tokens * topk) * (align - 1), rounded up to align; -1 for
+ * sizes out of range (0 <= tokens, 1 <= topk <= 64, 1 <= experts <= 1024,
+ * 1 <= align <= 1024, tokens * topk <= 2^26).  Pure host code. */
+int64_t mxa2a_moe_rows(int64_t tokens, int topk, int experts, int align);
+
+/* Stable sort of the assignments by expert.  expert: int32 [tokens][topk]
+ * (device); an id outside [0, experts) is an assignment that goes nowhere.
+ * Writes offsets int32 [experts + 1], counts int32 [experts], pos int32
+ * [tokens][topk] (the assignment's row, -1 if it goes nowhere) and, unless
+ * NULL, src int32 [rows] (the row's assignment token * topk + j, -1 for padding
+ * and past the last segment).  Within an expert, assignments keep their order.
+ * rows >= mxa2a_moe_rows(...), below 2^31. */
+int mxa2a_moe_sort(int64_t tokens, int topk, int experts, int align, int64_t rows, const void *expert,
+                   void *offsets, void *counts, void *pos, void *src, void *stream);
+
+/* Token rows into expert order: out[pos[t][j]] = x[t] for every assignment, and
+ * zeros in the segments' padding.  x: [tokens][hidden] of x_type (BF16, F16,
+ * F32), row stride ldx elements.  out: [rows][hidden] of out_type, which is
+ * x_type, or E4M3 / E5M2 with out_scale its scale tiles
+ * [ceil(hidden/128)][ceil(rows/128)][512] (hidden % 32 == 0; x, and ldx in
+ * bytes, 16-byte aligned; out 16-byte and out_scale 4-byte aligned).
+ * The gradient with respect to x is mxa2a_moe_combine of the rows' gradient
+ * with weight NULL. */
+int mxa2a_moe_dispatch(int64_t tokens, int topk, int experts, int64_t hidden, int64_t rows, const void *x, int x_type,
+                       int64_t ldx, const void *pos, const void *offsets, const void *counts, void *out, int out_type,
+                       void *out_scale, void *stream);
+
+/* The rows back in token order: out[t] = residual[t] + sum_j weight[t][j] *
+ * y[pos[t][j]], over the assignments that have a row.  y [rows][hidden],
+ * residual (NULL: none) and out [tokens][hidden] of type BF16, F16 or F32;
+ * weight fp32 [tokens][topk], NULL for 1. */
+int mxa2a_moe_combine(int64_t tokens, int topk, int64_t hidden, int64_t rows, const void *y, int type, const void *pos,
+                      const void *weight, const void *residual, void *out, void *stream);
+
+/* The combine's gradient: dy[pos[t][j]] = weight[t][j] * dout[t] and zeros in
+ * the padding, dweight[t][j] = sum_h dout[t][h] * y[pos[t][j]][h] (0 without a
+ * row).  dout [tokens][hidden], y and dy [rows][hidden] of `type`; weight
+ * (NULL: 1) and dweight fp32 [tokens][topk].  The residual's gradient is dout. */
+int mxa2a_moe_combine_backward(int64_t tokens, int topk, int experts, int64_t hidden, int64_t rows, const void *dout,
+                               int type, const void *y, const void *pos, const void *offsets, const void *counts,
+                               const void *weight, void *dy, void *dweight, void *stream);
+
+/* Bytes of the scale tiles of a [rows][cols] matrix. */
+int64_t mxa2a_scale_tiles_bytes(int64_t rows, int64_t cols);
+
+/* Plain E8M0 scales uint8 [groups][rows][cols/32] into scale tiles
+ * [groups][ceil(cols/128)][ceil(rows/128)][512] (bytes that stand for no
+ * element are 0).  cols % 32 == 0; tiles 4-byte aligned. */
+int mxa2a_scale_tiles(const void *scale, int groups, int64_t rows, int64_t cols, void *tiles, void *stream);
+
+/* MXFP8 quantisation of x [groups][rows][cols] (BF16, F16 or F32; row stride ldx
+ * elements, group stride rows * ldx; 16-byte aligned rows) with elements `format`
+ * (E4M3 or E5M2), read once for either or both of
+ *   codes [groups][rows][cols], scale: blocks along the columns (cols % 32 == 0);
+ *   codes_t [groups][cols][rows32], scale_t: the transpose, blocks along the
+ *     rows, rows32 = rows rounded up to 32 (the added codes are 0), its scale
+ *     tiles [groups][ceil(rows/128)][ceil(cols/128)][512];
+ * a pair of NULLs leaves that one out.  cols % 32 == 0 in either case; codes
+ * 16-byte aligned, scale tiles 4-byte. */
+int mxa2a_quantize(const void *x, int x_type, int64_t ldx, int groups, int64_t rows, int64_t cols, int format,
+                   void *codes, void *scale, void *codes_t, void *scale_t, void *stream);
+
+/* A linear layer with MXFP8 operands, one weight matrix per expert (groups = 1:
+ * an ordinary layer).  The plan owns what a call needs beside its arguments: the
+ * status block and, with training != 0, the quantised gradient of max_rows rows.
+ * 1 <= groups <= 1024; 1 <= max_rows <= 2^22; N, K multiples of 32, at most 2^20;
+ * groups * N, groups * K < 2^31.  One plan must not run on two streams at once.
+ * Returns NULL on error (mxa2a_last_error). */
+typedef struct mxa2a_linear mxa2a_linear;   /* opaque */
+int mxa2a_linear_validate(int groups, int64_t max_rows, int64_t N, int64_t K);
+mxa2a_linear *mxa2a_linear_create(int groups, int64_t max_rows, int64_t N, int64_t K, int training);
+
+/* out[t][n] = act( sum_k x[t][k] * w[g][n][k] + bias[g][n] ) + residual[t][n]
+ * for every row t of segment g, in one launch.
+ *   x [rows][K] codes and x_scale its scale tiles; w [groups][N][K] codes and
+ *   w_scale [groups][ceil(K/128)][ceil(N/128)][512] (E4M3 both, or
+ *   MXA2A_OPT_ELEM_TYPES); rows <= max_rows.
+ *   offsets, counts: the segments of the sort; their alignment must be a
+ *   multiple of 32.  NULL (both; groups == 1): all rows.
+ *   bias fp32 [groups][N], residual bf16 [rows][N], preact bf16 [rows][N] (the
+ *   value before the activation, which the gradient reads): each may be NULL.
+ *   out [rows][N]: BF16, F32, or E4M3 / E5M2 codes with out_scale
+ *   [ceil(N/128)][ceil(rows/128)][512], ready to be the next layer's x (scale
+ *   bytes past N or for rows not written keep what they held).
+ * Rows in a segment's padding are written as zeros (out and preact).
+ * x, w, out, preact, residual and scale tiles 16-byte aligned.
+ * Errors beside the common ones: MXA2A_ERR_WRONG_DEVICE; a device time-out
+ * later through mxa2a_linear_get_status (out is then undefined). */
+int mxa2a_linear_run(mxa2a_linear *layer, int64_t rows, const void *x, const void *x_scale, const void *w,
+                     const void *w_scale, void *out, int out_type, void *out_scale, const void *offsets,
+                     const void *counts, const void *bias, int activation, const void *residual, void *preact,
+                     void *stream);
+
+/* The layer's gradient (a plan with training != 0).  With
+ * dz = dy * act'(preact) (0 outside the segments' tokens), in fp32:
+ *   dbias[g][n] = sum over segment g of dz[t][n]
+ *   dx[t][k]    = sum_n q_n(dz)[t][n] * w_t[g][k][n]
+ *   dw[g][n][k] = sum over segment g of q_t(dz)[t][n] * x_t[k][t]
+ * where q_n and q_t are dz in MXFP8 of grad_format (E4M3 or E5M2), blocks of 32
+ * along n and along t.  dy, preact bf16 [rows][N] (preact NULL: activation
+ * NONE); x_t [K][rows32] the transposed quantisation of the layer's input
+ * (mxa2a_quantize; its padding rows must be zeros or any numbers) with its tiles
+ * [ceil(rows/128)][ceil(K/128)][512]; w_t [groups][K][N] the weights quantised
+ * along N, tiles [groups][ceil(N/128)][ceil(K/128)][512].  dx bf16 [rows][K]
+ * (zeros in the padding), dw [groups][N][K] of dw_type (BF16 or F32; zeros for a
+ * group without tokens), dbias fp32 [groups][N]: each may be NULL, and what only
+ * it needs is then not read and may be NULL too.  The residual's gradient is dy.
+ * Alignment and errors as for mxa2a_linear_run; MXA2A_ERR_INVALID_OPTION for a
+ * plan without training. */
+int mxa2a_linear_backward(mxa2a_linear *layer, int64_t rows, const void *dy, const void *preact, int activation,
+                          int grad_format, const void *x_t, const void *x_t_scale, const void *w_t,
+                          const void *w_t_scale, void *dx, void *dw, int dw_type, void *dbias, const void *offsets,
+                          const void *counts, void *stream);
+
+/* The device status of a layer's runs (as mxa2a_get_status; role 2 TMA
+ * producer, 3 MMA issuer, 4 epilogue, 7 scale copy). */
+int mxa2a_linear_get_status(mxa2a_linear *layer, mxa2a_status *out);
+
+/* MXA2A_OPT_TIMEOUT_NS and MXA2A_OPT_ELEM_TYPES (A is x, B is w), and, for get
+ * only, MXA2A_INFO_LAUNCHES and MXA2A_INFO_WORKSPACE_BYTES. */
+int mxa2a_linear_set_option(mxa2a_linear *layer, int key, int64_t value);
+int mxa2a_linear_get_option(mxa2a_linear *layer, int key, int64_t *value);
+
+/* Free the plan (synchronises the device first). NULL is a no-op. */
+void mxa2a_linear_destroy(mxa2a_linear *layer);
+
 /* Free the plan's workspace (synchronises the device first). NULL is a no-op.
  * Passage: all_to_all_matmul.cpp (the launcher), the teardown after the
  * runs (aclshmem_free of the communication space, aclrtFree of the buffers). */
