@@ -13,7 +13,9 @@
 // into tensor memory (one warp per lane quarter), the warps from 8 on are the
 // epilogue.  A stage is one 128-wide block of the contraction: 128 P rows,
 // tile_q Q rows (128-byte swizzled) and their scale tiles.  CTAs are
-// persistent over tiles.  With few tiles a cluster of up to 8 CTAs shares a
+// persistent over tiles.  The widest tile is computed by CTA pairs: 256 P rows x
+// 256 Q rows, the even CTA issuing the MMAs of both; a tile's MMAs are only as
+// wide as its segment needs.  With few tiles a cluster of up to 8 CTAs shares a
 // tile's contraction: each accumulates its part, the partial tiles meet in
 // distributed shared memory and every CTA sums (in rank order) and finishes
 // its share of the columns, in the same launch.
@@ -50,17 +52,22 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 
 template <int TQ>
 struct LinCfg {
-    static constexpr int kStages = TQ == 256 ? 4 : (TQ == 128 ? 6 : 4);
+    // The CTA-pair kernel: two CTAs compute 256 P rows x 256 Q rows with one
+    // MMA stream (cta_group::2), each holding its 128 P rows and half of the Q
+    // rows, so a stage moves and reads a third less shared memory per MMA.
+    static constexpr bool kPair = TQ == 256;
+    static constexpr int kStages = TQ >= 128 ? 6 : 4;
     static constexpr int kCtasPerSm = TQ <= 64 ? 2 : 1;
     static constexpr int kEpiWarps = TQ >= 128 ? 8 : 4;
     static constexpr int kThreads = 256 + 32 * kEpiWarps;
-    static constexpr int kAccBufs = TQ == 256 ? 1 : 2;
+    static constexpr int kAccBufs = kPair ? 1 : 2;
     static constexpr int kQAtoms = TQ == 32 ? 1 : TQ / 128 + (TQ == 64 ? 2 : 1);   // scale tiles a Q tile may touch
     static constexpr int kQCols = TQ / 32 < 4 ? 4 : TQ / 32;                        // TMEM columns of its scales
     static constexpr uint32_t kSfCol = TQ * kAccBufs;
     static constexpr uint32_t kSfCols = 4 + kQCols;
     static constexpr uint32_t kTmem = TQ <= 32 ? 128 : (TQ == 64 ? 256 : 512);
-    static constexpr int kQBytes = TQ * 128;
+    static constexpr int kQRows = kPair ? 128 : TQ;                                 // Q rows this CTA holds of a tile
+    static constexpr int kQBytes = kQRows * 128;
     static constexpr int kColsPerWarp = TQ / (kEpiWarps / 4);
     static constexpr size_t oP = 0;
     static constexpr size_t oQ = oP + (size_t)kStages * kAStageBytes;
@@ -69,8 +76,8 @@ struct LinCfg {
     static constexpr size_t oCtl = oSfq + (size_t)kStages * kQAtoms * 512;
     static constexpr size_t ctl_bytes();
     static_assert(kSfCol + kStages * kSfCols <= kTmem, "tensor memory columns");
-    // a split tile's fp32 partial [TQ][128] lies over the P stages, which its MMAs have read
-    static_assert(TQ * 512 <= kStages * (kAStageBytes + kQBytes), "partial tile");
+    // a split tile's fp32 partial [TQ][128] lies over the stages, which its MMAs have read
+    static_assert(kPair || TQ * 512 <= kStages * (kAStageBytes + kQBytes), "partial tile");
 };
 
 struct __align__(8) LinCtl {
@@ -85,7 +92,8 @@ struct __align__(8) LinCtl {
 template <int TQ>
 constexpr size_t LinCfg<TQ>::ctl_bytes() { return oCtl + sizeof(LinCtl) + 1024; }
 
-__device__ __noinline__ void lin_report(const LinParams& p, int role, long long parity) {
+// (inlined: a call would keep the register split below from being allocated)
+__device__ __forceinline__ void lin_report(const LinParams& p, int role, long long parity) {
     DevStatus* st = p.status;
     const unsigned long long mine = (p.launch_id << 8) | (unsigned long long)kErrTimeout;
     unsigned long long cur = atomicAdd(&st->key, 0ull);
@@ -105,11 +113,17 @@ __device__ __noinline__ void lin_report(const LinParams& p, int role, long long 
 
 // Bounded wait for an mbarrier phase.  After a time-out anywhere in the CTA
 // every later wait returns at once, so that all roles reach the end together.
+// kCluster: the phase is completed by arrivals from the other CTA of a pair.
+template <bool kCluster = false>
+__device__ __forceinline__ bool lin_try(uint64_t* bar, uint32_t parity) {
+    return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+template <bool kCluster = false>
 __device__ __forceinline__ void lin_wait(const LinParams& p, LinCtl* ctl, uint64_t* bar, uint32_t parity, int role) {
-    if (mbar_try_wait(bar, parity)) return;
+    if (lin_try<kCluster>(bar, parity)) return;
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait(bar, parity)) return;
+        if (lin_try<kCluster>(bar, parity)) return;
         if (ctl->abort) return;
         if ((n & 63) == 0 && globaltimer() - t0 > (uint64_t)p.timeout_ns) {
             lin_report(p, role, (long long)parity);
@@ -121,8 +135,9 @@ __device__ __forceinline__ void lin_wait(const LinParams& p, LinCtl* ctl, uint64
 
 struct LinItem {
     int group;
-    int p0;              // first P row inside the group
+    int p0;              // this CTA's first P row inside the group
     long long q0;        // first Q row
+    int nq;              // Q rows multiplied: up to the segment's end, a multiple of 32
     long long q_end;     // Q rows past this are not this tile's (segment end)
     long long q_live;    // Q rows past this are padding: zeros are written
     int b0, b1;          // 32-blocks of the contraction
@@ -162,11 +177,12 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
         it.group = lo;
         const int first = ctl->start[lo], qt = (ctl->start[lo + 1] - first) / p.pt;
         const int r = tile - first;
-        // bands of 16 P tiles, all Q tiles of a band before the next: the CTAs
+        // bands of 2048 P rows, all Q tiles of a band before the next: the CTAs
         // in flight share P and Q tiles in L2
-        const int band = r / (16 * qt), np = min(16, p.pt - band * 16), rb = r - band * 16 * qt;
+        constexpr int kBand = LinCfg<TQ>::kPair ? 8 : 16;
+        const int band = r / (kBand * qt), np = min(kBand, p.pt - band * kBand), rb = r - band * kBand * qt;
         q_tile = rb / np;
-        p_tile = band * 16 + rb - q_tile * np;
+        p_tile = band * kBand + rb - q_tile * np;
         long long o = 0;
         it.q_end = it.q_live = p.q_rows;
         if (p.offsets) {
@@ -179,11 +195,18 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
         it.b0 = 0;
         it.b1 = p.blocks;
     }
-    it.p0 = p_tile * 128;
+    it.p0 = p_tile * (LinCfg<TQ>::kPair ? 256 : 128) + (LinCfg<TQ>::kPair ? rank * 128 : 0);
+    it.nq = (int)min((long long)TQ, (it.q_end - it.q0 + 31) & ~31ll);
+    if (it.nq < 32) it.nq = 32;   // (a tile past its segment's end, which only foreign offsets make: nothing is stored)
     const int lo = it.b0 / 4, hi = it.b1 > it.b0 ? (it.b1 + 3) / 4 : lo;
-    const int per = (hi - lo + p.splits - 1) / p.splits;
-    it.kb0 = min(hi, lo + rank * per);
-    it.kb1 = min(hi, it.kb0 + per);
+    if (LinCfg<TQ>::kPair) {
+        it.kb0 = lo;
+        it.kb1 = hi;
+    } else {
+        const int per = (hi - lo + p.splits - 1) / p.splits;
+        it.kb0 = min(hi, lo + rank * per);
+        it.kb1 = min(hi, it.kb0 + per);
+    }
     return it;
 }
 
@@ -264,28 +287,45 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinItem& it,
     }
 }
 
+// columns of a warp's share that the pair kernel's epilogue finishes before it
+// releases the accumulator (the others wait in registers)
+constexpr int kDirectCols = 32;
+// registers: the pair kernel's epilogue keeps 96 columns of the accumulator; 8 warps x 168 + 8 x 88 are the launch's 16 x 128
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// arrive on a barrier of another CTA without ordering earlier generic-proxy
+// accesses (the caller's tensor-memory stores are complete: tcgen05.wait::st)
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 template <int TQ>
 __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     linear_kernel(const __grid_constant__ LinParams p, const __grid_constant__ CUtensorMap map_p,
-                  const __grid_constant__ CUtensorMap map_q) {
+                  const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q32) {
     using C = LinCfg<TQ>;
+    constexpr bool kPair = C::kPair;
     extern __shared__ uint8_t lin_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem_raw) + 1023) & ~uintptr_t(1023));
     LinCtl* ctl = reinterpret_cast<LinCtl*>(smem + C::oCtl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
-    const int first = (int)blockIdx.x / p.splits, stride = (int)gridDim.x / p.splits;
+    const bool split = !kPair && p.splits > 1;
+    const int share = kPair ? 2 : p.splits;      // CTAs to a tile
+    const int rank = kPair || split ? (int)cluster_ctarank() : 0;
+    const int first = (int)blockIdx.x / share, stride = (int)gridDim.x / share;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
             mbar_init(&ctl->sf_full[s], 1);
-            mbar_init(&ctl->sf_ready[s], 4);
+            mbar_init(&ctl->sf_ready[s], kPair ? 8 : 4);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->acc_full[b], 1);
-            mbar_init(&ctl->acc_empty[b], C::kEpiWarps);
+            mbar_init(&ctl->acc_empty[b], kPair ? 2 * C::kEpiWarps : C::kEpiWarps);
         }
         ctl->abort = 0;
         ctl->issued[0] = ctl->issued[1] = 0;
@@ -294,8 +334,13 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         prefetch_tensormap(&map_q);
     }
     if (warp == 1) {
-        tmem_alloc(&ctl->tmem, C::kTmem);
-        tmem_relinquish();
+        if (kPair) {
+            tmem_alloc_pair(&ctl->tmem, C::kTmem);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&ctl->tmem, C::kTmem);
+            tmem_relinquish();
+        }
     }
     if (warp == 3) {
         // first tile of every group
@@ -334,35 +379,59 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
     const int total = ctl->total;
-    const bool split = p.splits > 1;
 
-    if (split) cluster_sync();   // every CTA of the cluster runs before any reads its shared memory
+    if (kPair || split) cluster_sync();   // every CTA of the cluster runs before any touches its shared memory
 
+    // (whole warpgroups take each side; each side's code follows its register count)
+    if (warp < 8) {
+    if constexpr (kPair) regs_down<88>();
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------- TMA producers
         const int pid = warp / 2;
         int n = 0;
+        // (pair: both CTAs' loads of a stage complete on the even CTA's barrier,
+        // which its producer arms for the bytes of both)
+        const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
+        const uint64_t keep = l2_policy_evict_last();
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             const int qa = (int)(it.q0 >> 7);                                   // first scale tile of the Q rows
             const int atoms = min((int)((it.q0 & 127) + TQ + 127) >> 7, p.q_row_tiles - qa);
+            const int pa = min(it.p0 >> 7, p.p_row_tiles - 1);                  // (a pair's second half may lie past P)
+            const int py = (p.by_contraction ? 0 : it.group * p.p_rows) + it.p0;
+            const int half = it.nq / 2, boxes = (half + 31) / 32;               // pair: Q rows of each CTA, in boxes of 32
             if (lane == 0) {
                 for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                     if ((n & 1) != pid) continue;
                     const int stage = n % C::kStages;
-                    lin_wait(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma);
+                    lin_wait<kPair>(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma);
                     if (ctl->abort) break;
                     mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
                     bulk_load(smem + C::oSfp + stage * 512,
                               p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
-                                  ((size_t)kb * p.pt + it.p0 / 128) * 512,
+                                  ((size_t)kb * p.p_row_tiles + pa) * 512,
                               512, &ctl->sf_full[stage]);
                     bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512,
                               p.q_scale + ((size_t)kb * p.q_row_tiles + qa) * 512, 512 * atoms, &ctl->sf_full[stage]);
-                    mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
-                    tma_load_2d(smem + C::oP + (size_t)stage * kAStageBytes, &map_p, &ctl->full[stage], kb * 128,
-                                (p.by_contraction ? 0 : it.group * p.p_rows) + it.p0);
-                    tma_load_2d(smem + C::oQ + (size_t)stage * C::kQBytes, &map_q, &ctl->full[stage], kb * 128, (int)it.q0);
+                    uint8_t* pd = smem + C::oP + (size_t)stage * kAStageBytes;
+                    uint8_t* qd = smem + C::oQ + (size_t)stage * C::kQBytes;
+                    if constexpr (kPair) {
+                        const bool whole = it.nq == TQ;
+                        const uint32_t bytes = kAStageBytes + (whole ? C::kQBytes : boxes * 32 * 128);
+                        const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
+                        if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
+                        tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
+                        const int qy = (int)it.q0 + rank * half;
+                        if (whole)
+                            tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
+                        else
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d_pair(qd + b * 4096, &map_q32, bar, kb * 128, qy + b * 32, keep);
+                    } else {
+                        mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
+                        tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
+                        tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, (int)it.q0);
+                    }
                     ctl->issued[pid] = n + 1;
                 }
             }
@@ -373,23 +442,24 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             }
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA issuer
-        const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | ((uint32_t)(TQ >> 3) << 17) |
-                                (1u << 23) | (8u << 24);
+        // ---------------------------------------------------------- MMA issuer (pair: the even CTA's, for both)
+        const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | (1u << 23) | ((kPair ? 16u : 8u) << 24);
         int n = 0, acc = 0;
         for (int tile = first; tile < total; tile += stride) {
+            if (kPair && rank != 0) break;
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             if (lane == 0 && it.kb1 > it.kb0) {
                 const int buf = acc % C::kAccBufs;
-                lin_wait(p, ctl, &ctl->acc_empty[buf], ((acc / C::kAccBufs) & 1) ^ 1, kRoleMma);
+                lin_wait<kPair>(p, ctl, &ctl->acc_empty[buf], ((acc / C::kAccBufs) & 1) ^ 1, kRoleMma);
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * TQ);
+                const uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
                 uint32_t some = 0;
                 for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                     const int stage = n % C::kStages;
                     const uint32_t ph = (n / C::kStages) & 1;
-                    lin_wait(p, ctl, &ctl->full[stage], ph, kRoleMma);
-                    lin_wait(p, ctl, &ctl->sf_ready[stage], ph, kRoleMma);
+                    lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma);
+                    lin_wait<kPair>(p, ctl, &ctl->sf_ready[stage], ph, kRoleMma);
                     if (ctl->abort) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
@@ -398,13 +468,22 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (kb * 4 + k < it.b0 || kb * 4 + k >= it.b1) continue;
-                        mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc0 | ((uint32_t)k << 4) | ((uint32_t)k << 29), sf,
-                                     sf + 4, some);
+                        const uint32_t idesc = idesc1 | ((uint32_t)k << 4) | ((uint32_t)k << 29);
+                        if constexpr (kPair)
+                            mma_mxf8f6f4_pair(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
+                        else
+                            mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
                         some = 1;
                     }
-                    tc_commit(&ctl->empty[stage]);
+                    if constexpr (kPair)
+                        tc_commit_pair_multicast(&ctl->empty[stage], 0x3);
+                    else
+                        tc_commit(&ctl->empty[stage]);
                 }
-                tc_commit(&ctl->acc_full[buf]);
+                if constexpr (kPair)
+                    tc_commit_pair_multicast(&ctl->acc_full[buf], 0x3);
+                else
+                    tc_commit(&ctl->acc_full[buf]);
                 ++acc;
             }
             __syncwarp();
@@ -416,6 +495,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------- scale warps
         const int quarter = warp & 3;
+        const uint32_t ready0 = kPair ? mapa_shared(smem_u32(&ctl->sf_ready[0]), 0) : 0u;
         int n = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
@@ -447,7 +527,12 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->sf_ready[stage]);
+                if (lane == 0) {
+                    if (!kPair || rank == 0)
+                        mbar_arrive(&ctl->sf_ready[stage]);
+                    else
+                        mbar_arrive_remote_relaxed(ready0 + (uint32_t)stage * sizeof(uint64_t));
+                }
             }
             __syncwarp();
             if (split) {
@@ -455,8 +540,15 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 cluster_sync();
             }
         }
-    } else if (warp >= 8) {
+    } else if (split) {
+        for (int tile = first; tile < total; tile += stride) {
+            cluster_sync();
+            cluster_sync();
+        }
+    }
+    } else {
         // ---------------------------------------------------------- epilogue
+        if constexpr (kPair) regs_up<168>();
         const int quarter = warp & 3, part = (warp - 8) >> 2;
         float* partial = reinterpret_cast<float*>(smem);   // [TQ][128]: the split tiles' (over the stages)
         int acc = 0;
@@ -468,86 +560,140 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             const bool in_p = it.p0 + quarter * 32 < p.p_rows;   // (P rows come in blocks of 32: uniform over the warp)
             const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * TQ + part * C::kColsPerWarp);
             if (live) {
-                lin_wait(p, ctl, &ctl->acc_full[buf], (acc / C::kAccBufs) & 1, kRoleEpi);
+                lin_wait<kPair>(p, ctl, &ctl->acc_full[buf], (acc / C::kAccBufs) & 1, kRoleEpi);
                 __syncwarp();
                 tc_fence_after();
             }
+            if constexpr (kPair) {
+                // The first columns straight from the accumulator, the rest into
+                // registers, the accumulator released, then 16 columns at a time
+                // (the rest moves down: one copy of the code).
+                constexpr int kHeld = C::kColsPerWarp - kDirectCols;
+                const int cols = in_p ? it.nq - part * C::kColsPerWarp : 0;
+                float v[kHeld];
 #pragma unroll 1
-            for (int c = 0; c < C::kColsPerWarp; c += 16) {
-                float v[16];
+                for (int c = 0; c < C::kColsPerWarp; c += 16) {
+                    float u[16];
+                    if (c < kDirectCols) {
+                        if (live) {
+                            tmem_ld_32x32b_x16(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(u));
+                            tc_wait_ld();
+                        }
+                    } else {
+                        if (c == kDirectCols && live) {
+#pragma unroll
+                            for (int i = 0; i < kHeld; i += 32)
+                                tmem_ld_32x32b_x32(t + (uint32_t)(kDirectCols + i), *reinterpret_cast<uint32_t(*)[32]>(v + i));
+                            tc_wait_ld();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (rank == 0)
+                                    mbar_arrive(&ctl->acc_empty[buf]);
+                                else
+                                    mbar_arrive_remote(mapa_shared(smem_u32(&ctl->acc_empty[buf]), 0));
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = v[j];
+#pragma unroll
+                        for (int j = 0; j < kHeld - 16; ++j) v[j] = v[j + 16];
+                    }
+                    if (!live) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u[j] = 0.f;
+                    }
+                    if (c < cols) lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, u);
+                }
+                if (live) ++acc;
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < C::kColsPerWarp; c += 16) {
+                    float v[16];
+                    if (live) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(t + (uint32_t)c, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                    }
+                    if (split) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) partial[(part * C::kColsPerWarp + c + j) * 128 + quarter * 32 + lane] = v[j];
+                    } else if (in_p) {
+                        lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, v);
+                    }
+                }
                 if (live) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(t + (uint32_t)c, r);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
+                    ++acc;
                 }
                 if (split) {
+                    __syncwarp();
+                    cluster_sync();
+                    // this CTA's share of the columns, 4 at a time over the epilogue's column parts
+                    const int cols = TQ / p.splits, parts = C::kEpiWarps / 4;
+                    for (int c = rank * cols + part * 4; in_p && c < (rank + 1) * cols; c += 4 * parts) {
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int s = 0; s < p.splits; ++s) {
+                            const uint32_t at = mapa_shared(smem_u32(partial + c * 128 + quarter * 32 + lane), s);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) partial[(part * C::kColsPerWarp + c + j) * 128 + quarter * 32 + lane] = v[j];
-                } else if (in_p) {
-                    lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, v);
-                }
-            }
-            if (live) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
-                ++acc;
-            }
-            if (split) {
-                __syncwarp();
-                cluster_sync();
-                // this CTA's share of the columns, 4 at a time over the epilogue's column parts
-                const int share = TQ / p.splits, parts = C::kEpiWarps / 4;
-                for (int c = rank * share + part * 4; in_p && c < (rank + 1) * share; c += 4 * parts) {
-                    float v[4] = {0.f, 0.f, 0.f, 0.f};
-                    for (int s = 0; s < p.splits; ++s) {
-                        const uint32_t at = mapa_shared(smem_u32(partial + c * 128 + quarter * 32 + lane), s);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(ld_shared_cluster_u32(at + j * 512));
+                            for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(ld_shared_cluster_u32(at + j * 512));
+                        }
+                        lin_store<4>(p, it, f, lane, it.q0 + c, v);
                     }
-                    lin_store<4>(p, it, f, lane, it.q0 + c, v);
+                    fence_proxy_async_shared();   // (this thread's writes, before TMA fills the stages again)
+                    __syncwarp();
+                    cluster_sync();   // the partial tiles have been read: the stages may be filled again
                 }
-                fence_proxy_async_shared();   // (this thread's writes, before TMA fills the stages again)
-                __syncwarp();
-                cluster_sync();   // the partial tiles have been read: the stages may be filled again
             }
-        }
-    } else if (split) {
-        for (int tile = first; tile < total; tile += stride) {
-            cluster_sync();
-            cluster_sync();
         }
     }
     __syncthreads();
     if (ctl->abort && threadIdx.x == 0) {
         // loads may still be in flight into this CTA's shared memory: give them
-        // time to land (bounded) before the CTA ends
+        // time to land (bounded) before the CTA ends (pair: the even CTA's
+        // barrier counts both CTAs' loads, and both end together below)
         const uint64_t t0 = globaltimer();
         for (int s = 0; s < C::kStages; ++s) {
             const int last = max(ctl->issued[0], ctl->issued[1]) - 1;
             const int n = last - ((last - s) % C::kStages + C::kStages) % C::kStages;   // stage s's last use
             if (n < 0) continue;
-            while (!(mbar_try_wait(&ctl->full[s], (n / C::kStages) & 1) && mbar_try_wait(&ctl->sf_full[s], (n / C::kStages) & 1)))
+            while (!((kPair && rank != 0) || lin_try<kPair>(&ctl->full[s], (n / C::kStages) & 1)) ||
+                   !mbar_try_wait(&ctl->sf_full[s], (n / C::kStages) & 1))
                 if (globaltimer() - t0 > (uint64_t)p.timeout_ns) break;
         }
     }
     __syncthreads();
+    if (kPair) cluster_sync();   // both CTAs are done with each other's barriers and tensor memory
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
+        if (kPair)
+            tmem_dealloc_pair(tmem, C::kTmem);
+        else
+            tmem_dealloc(tmem, C::kTmem);
     }
 }
 
 template <int TQ>
-cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas, cudaStream_t stream) {
+cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q32, int ctas,
+                      cudaStream_t stream) {
     using C = LinCfg<TQ>;
-    cudaError_t e = cudaFuncSetAttribute(linear_kernel<TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ctl_bytes());
+    // (once per device: the call costs more than the launch)
+    static unsigned long long ready = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
+        e = cudaFuncSetAttribute(linear_kernel<TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ctl_bytes());
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(C::kThreads);
@@ -555,21 +701,21 @@ cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtens
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)p.splits, 1, 1};
+    at[0].val.clusterDim = {(unsigned)(C::kPair ? 2 : p.splits), 1, 1};
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<TQ>, p, map_p, map_q);
+    cfg.numAttrs = C::kPair || p.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_kernel<TQ>, p, map_p, map_q, map_q32);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas,
-                          cudaStream_t stream) {
+cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q,
+                          const CUtensorMap& map_q32, int ctas, cudaStream_t stream) {
     switch (tile_q) {
-        case 32: return launch_tq<32>(p, map_p, map_q, ctas, stream);
-        case 64: return launch_tq<64>(p, map_p, map_q, ctas, stream);
-        case 128: return launch_tq<128>(p, map_p, map_q, ctas, stream);
-        default: return launch_tq<256>(p, map_p, map_q, ctas, stream);
+        case 32: return launch_tq<32>(p, map_p, map_q, map_q32, ctas, stream);
+        case 64: return launch_tq<64>(p, map_p, map_q, map_q32, ctas, stream);
+        case 128: return launch_tq<128>(p, map_p, map_q, map_q32, ctas, stream);
+        default: return launch_tq<256>(p, map_p, map_q, map_q32, ctas, stream);
     }
 }
 

@@ -22,6 +22,7 @@ struct LinParams {
     int p_rows, q_rows;        // rows of P per group; rows of Q
     int blocks;                // 32-blocks along the contraction
     int pt, qt;                // tiles of P per group; by_contraction: tiles of Q
+    int p_row_tiles;           // 128-row tiles of one group's P scale array
     int q_row_tiles;           // 128-row tiles of Q's scale array
     int splits;                // CTAs of a cluster that share a tile's contraction (1, 2, 4, 8)
     int fmt_p, fmt_q;          // MMA element codes: 0 E4M3, 1 E5M2
@@ -44,9 +45,14 @@ struct LinParams {
 
 constexpr int kRoleScale = 7;
 
-// tile_q: 32, 64, 128 or 256.  ctas: CTAs to launch (a multiple of splits)
-cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q, int ctas,
-                          cudaStream_t stream);
+// tile_q: 32, 64, 128, or 256 (the CTA-pair kernel: 256 P rows to a tile, ctas
+// in pairs, no splits).  map_q: boxes of linear_q_box(tile_q) rows; map_q32
+// (tile_q 256 only): boxes of 32 rows.  ctas: CTAs to launch, a multiple of
+// splits (of 2 for pairs)
+cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q,
+                          const CUtensorMap& map_q32, int ctas, cudaStream_t stream);
+inline int linear_q_box(int tile_q) { return tile_q == 256 ? 128 : tile_q; }
+inline int linear_p_tile(int tile_q) { return tile_q == 256 ? 256 : 128; }
 // CTAs of the kernel that one SM holds at once
 int linear_ctas_per_sm(int tile_q);
 

@@ -312,7 +312,15 @@ template <typename Tiles>
 Shape choose_shape(int sms, double tokens, int kblocks, Tiles tiles) {
     Shape s;
     s.tq = tokens * 1.2 <= 32 ? 32 : tokens * 1.2 <= 64 ? 64 : tokens * 1.2 <= 128 ? 128 : 256;
-    while (s.tq > 128 && tiles(s.tq) < sms) s.tq /= 2;
+    if (s.tq == 256) {
+        s.splits = 1;
+        const int64_t pairs = std::min<int64_t>(tiles(256), sms / 2);
+        if (pairs == sms / 2) {
+            s.ctas = (int)pairs * 2;
+            return s;
+        }
+        s.tq = 128;   // fewer pair tiles than pairs: single CTAs on narrower tiles
+    }
     const int64_t slots = (int64_t)sms * linear_ctas_per_sm(s.tq), n = std::max<int64_t>(1, tiles(s.tq));
     s.splits = 1;
     while (s.splits < 8 && n * s.splits * 2 <= slots && kblocks / (s.splits * 2) >= 2) s.splits *= 2;
@@ -335,7 +343,7 @@ int launch_product(mxa2a_linear* l, const Product& d, LinParams p, cudaStream_t 
     p.p_rows = (int)d.p_rows;
     p.q_rows = (int)d.q_rows;
     p.blocks = (int)(d.cols / 32);
-    p.pt = (int)((d.p_rows + 127) / 128);
+    p.p_row_tiles = (int)((d.p_rows + 127) / 128);
     p.q_row_tiles = (int)((d.q_rows + 127) / 128);
     p.p_scale = static_cast<const uint8_t*>(d.p_scale);
     p.q_scale = static_cast<const uint8_t*>(d.q_scale);
@@ -343,23 +351,26 @@ int launch_product(mxa2a_linear* l, const Product& d, LinParams p, cudaStream_t 
     p.status = l->status;
     p.timeout_ns = l->timeout_ns;
     const int kblocks = (int)((d.cols + 127) / 128);
-    const int64_t pt = p.pt, groups = d.groups, q = d.q_rows;
+    const int64_t groups = d.groups, q = d.q_rows;
     const bool by_c = d.by_contraction != 0, segs = p.offsets != nullptr;
     const Shape s = choose_shape(l->sms, d.tokens, by_c ? std::max<int>(1, (int)(kblocks / groups)) : kblocks, [&](int tq) {
-        const int64_t whole = (q + tq - 1) / tq;
+        const int64_t whole = (q + tq - 1) / tq, pt = (d.p_rows + linear_p_tile(tq) - 1) / linear_p_tile(tq);
         if (by_c) return groups * pt * whole;
         // (a group's last tile may be partly filled; a group without rows has none)
         return pt * (segs ? std::min(q / tq + std::min<int64_t>(groups, q / 32), (q + 31) / 32) : whole);
     });
+    p.pt = (int)((d.p_rows + linear_p_tile(s.tq) - 1) / linear_p_tile(s.tq));
     p.qt = (int)((q + s.tq - 1) / s.tq);
     p.splits = s.splits;
-    CUtensorMap mp, mq;
+    CUtensorMap mp, mq, mq32;
     if (!encode_2d(&mp, d.p, (uint64_t)d.cols, (uint64_t)(d.p_groups * d.p_rows), 128) ||
-        !encode_2d(&mq, d.q, (uint64_t)d.cols, (uint64_t)d.q_rows, (uint32_t)s.tq))
+        !encode_2d(&mq, d.q, (uint64_t)d.cols, (uint64_t)d.q_rows, (uint32_t)linear_q_box(s.tq)) ||
+        (s.tq == 256 && !encode_2d(&mq32, d.q, (uint64_t)d.cols, (uint64_t)d.q_rows, 32)))
         return MXA2A_ERR_CUDA;
+    if (s.tq != 256) mq32 = mq;
     p.launch_id = ++l->launch_id;
     ++l->launches;
-    return cuda_code(launch_linear(p, s.tq, mp, mq, s.ctas, stream));
+    return cuda_code(launch_linear(p, s.tq, mp, mq, mq32, s.ctas, stream));
 }
 
 // tokens of a group, from the row capacity that the caller gave: every segment may hold up to 31 rows of padding

@@ -196,19 +196,31 @@ def strerror(code: int) -> str:
 def _ptr(x) -> int:
     if x is None:
         return 0
+    try:
+        return x.data_ptr()      # (a torch tensor: the usual case first, a decode step makes many calls)
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(x)}")
 
 
+_current_stream = None
+
+
 def _stream(s) -> int:
+    global _current_stream
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            if raw is not None:   # the stream's handle without making a torch.cuda.Stream (some microseconds)
+                _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+            else:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
