@@ -210,56 +210,117 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
     return it;
 }
 
-// ------------------------------------------------------------------ epilogue of NC columns
-// v[j]: the sums of this lane's feature (P row `f`) for tokens q + j.
+// ------------------------------------------------------------------ epilogue
+// A warp's share of a tile: lanes are 32 consecutive features (P rows), columns
+// consecutive tokens (Q rows).
+struct LinShare {
+    long long row;   // output row of the share's first column
+    int end, live;   // columns from the first one on that are written / that hold tokens (the others are zeros)
+    int f;           // this lane's feature
+    float bias;
+};
+__device__ __forceinline__ LinShare lin_share(const LinParams& p, const LinItem& it, int f, int col0) {
+    LinShare e;
+    const long long q = it.q0 + col0;
+    e.row = (p.by_contraction ? (long long)it.group * p.q_rows : 0) + q;
+    e.end = (int)max(0ll, it.q_end - q);
+    e.live = (int)max(0ll, min(it.q_live - q, (long long)e.end));
+    e.f = f;
+    e.bias = p.bias && f < p.p_rows ? __ldg(p.bias + (size_t)it.group * p.p_rows + f) : 0.f;
+    return e;
+}
+
+// BF16 values of two tokens and this lane's feature <-> one token and two
+// features (even lanes the first token): one exchange with the neighbouring lane
+__device__ __forceinline__ uint32_t lin_swap(uint32_t w, int lane) {
+    return __byte_perm(w, __shfl_xor_sync(kLanes, w, 1), lane & 1 ? 0x3276 : 0x5410);
+}
+// (A piece inside the segment takes the path without a comparison per store,
+// its addresses by addition: the products and comparisons of the other path are
+// most of its instructions, 1.7 us against 0.7 us for 32 columns.)
 template <int NC>
-__device__ __forceinline__ void lin_store(const LinParams& p, const LinItem& it, int f, int lane, long long q, float (&v)[NC]) {
-    static_assert(NC % 4 == 0, "columns");
-    if (q >= it.q_end) return;   // (uniform over the warp)
-    const long long row0 = (p.by_contraction ? (long long)it.group * p.q_rows : 0) + q;
-    const bool odd = lane & 1;
-    const float b = p.bias ? __ldg(p.bias + (size_t)it.group * p.p_rows + f) : 0.f;
-    uint16_t* const pre = p.preact;
-    const int fe = f & ~1;       // the feature pair this lane stores
+__device__ __forceinline__ void lin_store_bf16(uint16_t* out, int ld, const LinShare& e, int j0, int lane, const float (&v)[NC]) {
+    const int odd = lane & 1;
+    char* o = reinterpret_cast<char*>(out + (e.row + j0 + odd) * ld + (e.f & ~1));
+    const size_t step = (size_t)ld * 4;   // two rows
+    if (j0 + NC <= e.end) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] = q + j < it.q_live ? v[j] + b : 0.f;
-    if (pre) {
+        for (int j = 0; j < NC; j += 2, o += step)
+            *reinterpret_cast<uint32_t*>(o) = lin_swap(bf16x2_bits(v[j], v[j + 1]), lane);
+    } else {
+        const int left = e.end - j0 - odd;
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-            const float got = __shfl_xor_sync(kLanes, odd ? v[j] : v[j + 1], 1);
-            const uint32_t w = odd ? bf16x2_bits(got, v[j + 1]) : bf16x2_bits(v[j], got);
-            if (q + j + odd < it.q_end) *reinterpret_cast<uint32_t*>(pre + (row0 + j + odd) * p.p_rows + fe) = w;
+        for (int j = 0; j < NC; j += 2, o += step) {
+            const uint32_t w = lin_swap(bf16x2_bits(v[j], v[j + 1]), lane);
+            if (j < left) *reinterpret_cast<uint32_t*>(o) = w;
         }
     }
-    if (p.act != kActNone) {
+}
+
+// Finish columns j0 .. j0 + NC - 1 of the share: v[j] are their sums.
+template <int NC>
+__device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e, int j0, int lane, float (&v)[NC]) {
+    static_assert(NC % 4 == 0, "columns");
+    if (j0 >= e.end) return;   // (uniform over the warp)
+    const int ld = p.p_rows;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], p.act);   // (0 stays 0 on padding rows)
+    for (int j = 0; j < NC; ++j) v[j] += e.bias;
+    if (j0 + NC > e.live) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = j0 + j < e.live ? v[j] : 0.f;
+    }
+    if (p.preact) lin_store_bf16<NC>(p.preact, ld, e, j0, lane, v);
+    // (0 stays 0 on padding rows)
+    if (p.act == kActGelu) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActGelu);
+    } else if (p.act == kActSilu) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActSilu);
+    } else if (p.act == kActRelu) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActRelu);
     }
     if (p.residual) {
+        const int odd = lane & 1, left = e.live - j0 - odd;
+        const char* r = reinterpret_cast<const char*>(p.residual + (e.row + j0 + odd) * ld + (e.f & ~1));
+        const size_t step = (size_t)ld * 4;
+        uint32_t w[NC / 2];
+        if (j0 + NC <= e.live) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-            if (q + j < it.q_live) v[j] += __uint_as_float((uint32_t)__ldg(p.residual + (row0 + j) * p.p_rows + f) << 16);
-    }
-    if (p.out_type == kTypeBf16) {
-        uint16_t* out = static_cast<uint16_t*>(p.out);
+            for (int j = 0; j < NC; j += 2, r += step) w[j / 2] = __ldg(reinterpret_cast<const uint32_t*>(r));
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; j += 2, r += step)
+                w[j / 2] = j < left ? __ldg(reinterpret_cast<const uint32_t*>(r)) : 0u;
+        }
 #pragma unroll
         for (int j = 0; j < NC; j += 2) {
-            const float got = __shfl_xor_sync(kLanes, odd ? v[j] : v[j + 1], 1);
-            const uint32_t w = odd ? bf16x2_bits(got, v[j + 1]) : bf16x2_bits(v[j], got);
-            if (q + j + odd < it.q_end) *reinterpret_cast<uint32_t*>(out + (row0 + j + odd) * p.p_rows + fe) = w;
+            const uint32_t t = lin_swap(w[j / 2], lane);
+            v[j] += bf16_lo(t);
+            v[j + 1] += bf16_hi(t);
         }
+    }
+    if (p.out_type == kTypeBf16) {
+        lin_store_bf16<NC>(static_cast<uint16_t*>(p.out), ld, e, j0, lane, v);
     } else if (p.out_type == kTypeF32) {
-        float* out = static_cast<float*>(p.out);
+        float* o = static_cast<float*>(p.out) + (e.row + j0) * ld + e.f;
+        if (j0 + NC <= e.end) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-            if (q + j < it.q_end) out[(row0 + j) * p.p_rows + f] = v[j];
+            for (int j = 0; j < NC; ++j, o += ld) *o = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; ++j, o += ld)
+                if (j0 + j < e.end) *o = v[j];
+        }
     } else {
         // the warp's 32 features are one MX block of every token
         uint8_t* out = static_cast<uint8_t*>(p.out);
         const bool e5m2 = p.out_type == kTypeE5M2;
-        const int emax = mx_emax(e5m2), kb = f >> 7;
+        const int emax = mx_emax(e5m2), kb = e.f >> 7, i3 = lane & 3;
+        uint8_t* o = out + (e.row + j0 + i3) * ld + (e.f & ~3);
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
+        for (int j = 0; j < NC; j += 4, o += 4 * (size_t)ld) {
             float s[4];
             uint32_t bytes = 0, nan = 0;
 #pragma unroll
@@ -273,15 +334,12 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinItem& it,
             // (a NaN block's codes are all NaN)
             w = (w & ~((nan >> 6 & 0x01010101u) * 0xffu)) | nan;
             // 4 x 4 byte transpose over four lanes: lane 4 a + i then holds features 4 a .. 4 a + 3 of token j + i
-            const uint32_t o1 = __shfl_xor_sync(kLanes, w, 1);
-            w = odd ? __byte_perm(o1, w, 0x7351) : __byte_perm(w, o1, 0x6240);
-            const uint32_t o2 = __shfl_xor_sync(kLanes, w, 2);
-            w = (lane & 2) ? __byte_perm(o2, w, 0x7632) : __byte_perm(w, o2, 0x5410);
-            const int i = lane & 3;
-            if (q + j + i < it.q_end) {
-                *reinterpret_cast<uint32_t*>(out + (row0 + j + i) * p.p_rows + (f & ~3)) = w;
+            w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 1), lane & 1 ? 0x3715 : 0x6240);
+            w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 2), lane & 2 ? 0x3276 : 0x5410);
+            if (j0 + j + i3 < e.end) {
+                *reinterpret_cast<uint32_t*>(o) = w;
                 if (lane < 4)
-                    p.out_scale[scale_word(kb, row0 + j + i, p.q_row_tiles) + ((f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i));
+                    p.out_scale[scale_word(kb, e.row + j0 + j + i3, p.q_row_tiles) + ((e.f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i3));
             }
         }
     }
@@ -295,8 +353,9 @@ template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-// arrive on a barrier of another CTA without ordering earlier generic-proxy
-// accesses (the caller's tensor-memory stores are complete: tcgen05.wait::st)
+// arrive on a barrier of another CTA without ordering earlier memory accesses (a
+// release waits for every earlier global store, about 1 us; what the barrier
+// hands over is tensor memory, whose accesses are complete: tcgen05.wait::st / ::ld)
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -564,19 +623,19 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 __syncwarp();
                 tc_fence_after();
             }
+            const LinShare e = lin_share(p, it, f, part * C::kColsPerWarp);
             if constexpr (kPair) {
                 // The first columns straight from the accumulator, the rest into
-                // registers, the accumulator released, then 16 columns at a time
+                // registers, the accumulator released, then 32 columns at a time
                 // (the rest moves down: one copy of the code).
                 constexpr int kHeld = C::kColsPerWarp - kDirectCols;
-                const int cols = in_p ? it.nq - part * C::kColsPerWarp : 0;
                 float v[kHeld];
 #pragma unroll 1
-                for (int c = 0; c < C::kColsPerWarp; c += 16) {
-                    float u[16];
+                for (int c = 0; c < C::kColsPerWarp; c += 32) {
+                    float u[32];
                     if (c < kDirectCols) {
                         if (live) {
-                            tmem_ld_32x32b_x16(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(u));
+                            tmem_ld_32x32b_x32(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(u));
                             tc_wait_ld();
                         }
                     } else {
@@ -591,19 +650,19 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                                 if (rank == 0)
                                     mbar_arrive(&ctl->acc_empty[buf]);
                                 else
-                                    mbar_arrive_remote(mapa_shared(smem_u32(&ctl->acc_empty[buf]), 0));
+                                    mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&ctl->acc_empty[buf]), 0));
                             }
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = v[j];
+                        for (int j = 0; j < 32; ++j) u[j] = v[j];
 #pragma unroll
-                        for (int j = 0; j < kHeld - 16; ++j) v[j] = v[j + 16];
+                        for (int j = 0; j < kHeld - 32; ++j) v[j] = v[j + 32];
                     }
                     if (!live) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) u[j] = 0.f;
+                        for (int j = 0; j < 32; ++j) u[j] = 0.f;
                     }
-                    if (c < cols) lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, u);
+                    if (in_p) lin_store<32>(p, e, c, lane, u);
                 }
                 if (live) ++acc;
             } else {
@@ -624,7 +683,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) partial[(part * C::kColsPerWarp + c + j) * 128 + quarter * 32 + lane] = v[j];
                     } else if (in_p) {
-                        lin_store<16>(p, it, f, lane, it.q0 + part * C::kColsPerWarp + c, v);
+                        lin_store<16>(p, e, c, lane, v);
                     }
                 }
                 if (live) {
@@ -638,6 +697,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     cluster_sync();
                     // this CTA's share of the columns, 4 at a time over the epilogue's column parts
                     const int cols = TQ / p.splits, parts = C::kEpiWarps / 4;
+                    const LinShare whole = lin_share(p, it, f, 0);
                     for (int c = rank * cols + part * 4; in_p && c < (rank + 1) * cols; c += 4 * parts) {
                         float v[4] = {0.f, 0.f, 0.f, 0.f};
                         for (int s = 0; s < p.splits; ++s) {
@@ -645,7 +705,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(ld_shared_cluster_u32(at + j * 512));
                         }
-                        lin_store<4>(p, it, f, lane, it.q0 + c, v);
+                        lin_store<4>(p, whole, c, lane, v);
                     }
                     fence_proxy_async_shared();   // (this thread's writes, before TMA fills the stages again)
                     __syncwarp();

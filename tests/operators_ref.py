@@ -67,10 +67,11 @@ def quant_values(x, fmt):
     return q * np.repeat(np.exp2(X), 32, axis=-1)
 
 
-def tie_slack(x, fmt, rel):
-    """Per element: how far its quantised value may move when the element moves by rel of itself (a neighbouring
-    code, or the whole block where its largest magnitude is that near a power of two)."""
-    lo, hi = quant_values(x * (1 - rel), fmt), quant_values(x * (1 + rel), fmt)
+def tie_slack(x, fmt, err):
+    """Per element: how far its quantised value may move when the element moves by err (a neighbouring code, or the
+    whole block where its largest magnitude is that near a power of two)."""
+    sign = np.where(x < 0, -1.0, 1.0)
+    lo, hi = quant_values(x - sign * err, fmt), quant_values(x + sign * err, fmt)
     return np.abs(hi - lo)
 
 
@@ -125,6 +126,18 @@ def slope(z, name):
         s = 1 / (1 + np.exp(-z))
         return s * (1 + z * (1 - s))
     return np.ones_like(z)
+
+
+def slope_size(z, name):
+    """Sum of the magnitudes of the two terms that slope() adds (they cancel near gelu's and silu's lowest point)."""
+    if name == "gelu":
+        a = math.sqrt(2 / math.pi)
+        s = 0.5 * (1 + np.tanh(a * (z + 0.044715 * z ** 3)))
+        return s + np.abs(slope(z, name) - s)
+    if name == "silu":
+        s = 1 / (1 + np.exp(-z))
+        return s + np.abs(slope(z, name) - s)
+    return np.abs(slope(z, name))
 
 
 def f64(t):

@@ -5,8 +5,10 @@ terms in fp32 on the tensor cores, whose additions may truncate: at most K units
 of 2^-23 of the sum of magnitudes.  Bias, activation (slope at most 1.13, a few
 fp32 roundings) and residual add 8 half-ulps of their sizes, the output its
 rounding.  MXFP8 outputs lie between the codes of the two ends of that interval.
-A gradient's quantised dz may take a neighbouring code where dz in fp32 (2^-19 of
-itself: its activation's slope sums a few terms) is that near a tie.
+The slope of gelu and silu is a sum of two terms, each off by a few fp32
+roundings: dz is known to 2^-19 of |dy| times the sum of their magnitudes (they
+cancel at the lowest point of the curve, where no fp32 sum is exact to any part of
+itself).  A quantised dz may take a neighbouring code where it is that near a tie.
 """
 import numpy as np
 import pytest
@@ -211,6 +213,21 @@ def test_linear_grouped(lens, N, K, out):
     check_layer(i, out, act="silu", with_bias=True, with_residual=True, preact=True)
 
 
+# enough tiles for the CTA-pair kernel, segments starting at every 32-row place of a scale tile, an odd count of
+# 128-row weight tiles
+WIDE = [300, 0, 270, 33, 520, 1, 96]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32", "e4m3", "e5m2"])
+def test_linear_wide_grouped(out):
+    check_layer(layer_inputs(WIDE, 4128, 160, 2, slack=70), out, act="gelu", with_bias=True, with_residual=True, preact=True)
+
+
+@pytest.mark.parametrize("T,N,K", [(2500, 2080, 288), (257, 20000, 128), (4096, 1184, 1024)])
+def test_linear_wide_dense(T, N, K):
+    check_layer(layer_inputs([T], N, K, T, dense=True), act="silu", with_bias=True, with_residual=True)
+
+
 @pytest.mark.parametrize("align", [64, 128, 256])
 def test_linear_other_alignments(align):
     i = layer_inputs([3, 130, 0, 65], 96, 224, align, align=align)
@@ -292,23 +309,26 @@ def run_backward(i, act, fmt, dw="bf16", seed=1, want=("dx", "dw", "dbias"), lay
     torch.cuda.synchronize()
     assert l.status()["code"] == 0
     dz = np.where(live[:, None], np.nan_to_num(R.f64(dy)), 0)
+    err = np.zeros_like(dz)
     if act != "none":
-        dz = dz * np.where(live[:, None], R.slope(np.where(live[:, None], R.f64(z), 0), act), 0)
-    return o, dz, XT[2], WT[2], used
+        zv = np.where(live[:, None], R.f64(z), 0)
+        if act != "relu":
+            err = DZ_REL * np.abs(dz) * R.slope_size(zv, act)
+        dz = dz * np.where(live[:, None], R.slope(zv, act), 0)
+    return o, dz, err, XT[2], WT[2], used
 
 
 def check_backward(i, act, fmt, dw="bf16", want=("dx", "dw", "dbias"), layer=None):
-    o, dz, xt, wt, used = run_backward(i, act, fmt, dw, want=want, layer=layer)
-    rows, N, K, G = i["rows"], i["N"], i["K"], i["G"]
-    rel = 0.0 if act in ("none", "relu") else DZ_REL
-    pad = np.zeros((R.up(rows, 32), N))
-    pad[:rows] = dz
-    qn, sn = R.quant_values(dz, fmt), R.tie_slack(dz, fmt, rel)
-    qt, st = R.quant_values(pad.T.copy(), fmt), R.tie_slack(pad.T.copy(), fmt, rel)
+    o, dz, derr, xt, wt, used = run_backward(i, act, fmt, dw, want=want, layer=layer)
+    rows, N, K = i["rows"], i["N"], i["K"]
+    pad, perr = np.zeros((R.up(rows, 32), N)), np.zeros((R.up(rows, 32), N))
+    pad[:rows], perr[:rows] = dz, derr
+    qn, sn = R.quant_values(dz, fmt), R.tie_slack(dz, fmt, derr)
+    qt, st = R.quant_values(pad.T.copy(), fmt), R.tie_slack(pad.T.copy(), fmt, perr.T)
     for g, n in enumerate(i["lens"]):
         a, b = i["starts"][g], i["starts"][g] + n
         if o["dbias"] is not None:
-            R.check(o["dbias"][g], dz[a:b].sum(0), (n * R.F32_EPS * 1.01 + rel) * np.abs(dz[a:b]).sum(0), "dbias")
+            R.check(o["dbias"][g], dz[a:b].sum(0), n * R.F32_EPS * 1.01 * np.abs(dz[a:b]).sum(0) + derr[a:b].sum(0), "dbias")
         if o["dx"] is not None:
             ref = qn[a:b] @ wt[g].T
             err = N * 2.0 ** -23 * (np.abs(qn[a:b]) @ np.abs(wt[g]).T) + sn[a:b] @ np.abs(wt[g]).T
@@ -333,6 +353,13 @@ def test_backward_dense(T, N, K, act, fmt):
 def test_backward_grouped(lens, N, K):
     i = layer_inputs(lens, N, K, len(lens), slack=70)
     check_backward(i, "silu", "e4m3")
+    check_backward(i, "none", "e5m2", dw="f32")
+
+
+@pytest.mark.parametrize("lens,N,K", [(WIDE, 160, 4128), ([700, 801], 1184, 2080)])
+def test_backward_wide(lens, N, K):
+    i = layer_inputs(lens, N, K, 9, slack=70)
+    check_backward(i, "gelu", "e4m3")
     check_backward(i, "none", "e5m2", dw="f32")
 
 
