@@ -81,7 +81,9 @@ struct LinCfg {
 };
 
 struct __align__(8) LinCtl {
-    uint64_t full[kLinMaxStages], empty[kLinMaxStages], sf_full[kLinMaxStages], sf_ready[kLinMaxStages];
+    uint64_t full[kLinMaxStages];      // operands landed and scales in tensor memory
+    uint64_t empty[kLinMaxStages];     // the stage's MMAs are done
+    uint64_t sf_full[kLinMaxStages];   // scale tiles landed in shared memory
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
     volatile int abort;
@@ -377,10 +379,10 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&ctl->full[s], 1);
+            // the producer's arming and one arrival per scale warp
+            mbar_init(&ctl->full[s], 1 + (kPair ? 8 : 4));
             mbar_init(&ctl->empty[s], 1);
             mbar_init(&ctl->sf_full[s], 1);
-            mbar_init(&ctl->sf_ready[s], kPair ? 8 : 4);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->acc_full[b], 1);
@@ -518,7 +520,6 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     const int stage = n % C::kStages;
                     const uint32_t ph = (n / C::kStages) & 1;
                     lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma);
-                    lin_wait<kPair>(p, ctl, &ctl->sf_ready[stage], ph, kRoleMma);
                     if (ctl->abort) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------- scale warps
         const int quarter = warp & 3;
-        const uint32_t ready0 = kPair ? mapa_shared(smem_u32(&ctl->sf_ready[0]), 0) : 0u;
+        const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
         int n = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
@@ -588,9 +589,9 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 __syncwarp();
                 if (lane == 0) {
                     if (!kPair || rank == 0)
-                        mbar_arrive(&ctl->sf_ready[stage]);
+                        mbar_arrive(&ctl->full[stage]);
                     else
-                        mbar_arrive_remote_relaxed(ready0 + (uint32_t)stage * sizeof(uint64_t));
+                        mbar_arrive_remote_relaxed(full0 + (uint32_t)stage * sizeof(uint64_t));
                 }
             }
             __syncwarp();
