@@ -56,14 +56,19 @@ struct LinCfg {
     // MMA stream (cta_group::2), each holding its 128 P rows and half of the Q
     // rows, so a stage moves and reads a third less shared memory per MMA.
     static constexpr bool kPair = TQ == 256;
-    static constexpr int kStages = TQ >= 128 ? 6 : 4;
+    static constexpr int kStages = kPair ? 5 : (TQ == 128 ? 6 : 4);
     static constexpr int kCtasPerSm = TQ <= 64 ? 2 : 1;
     static constexpr int kEpiWarps = TQ >= 128 ? 8 : 4;
     static constexpr int kThreads = 256 + 32 * kEpiWarps;
-    static constexpr int kAccBufs = kPair ? 1 : 2;
+    // Two accumulators.  Two of 256 columns would leave none for the scales, so
+    // the pair kernel's overlap by 64 (columns 0..255 and 192..447): those are
+    // moved to registers before the next tile's MMAs start, the others are read
+    // while it runs.
+    static constexpr int kAccStep = kPair ? 192 : TQ;
+    static constexpr int kOverlap = TQ - kAccStep;
     static constexpr int kQAtoms = TQ == 32 ? 1 : TQ / 128 + (TQ == 64 ? 2 : 1);   // scale tiles a Q tile may touch
     static constexpr int kQCols = TQ / 32 < 4 ? 4 : TQ / 32;                        // TMEM columns of its scales
-    static constexpr uint32_t kSfCol = TQ * kAccBufs;
+    static constexpr uint32_t kSfCol = kAccStep + TQ;
     static constexpr uint32_t kSfCols = 4 + kQCols;
     static constexpr uint32_t kTmem = TQ <= 32 ? 128 : (TQ == 64 ? 256 : 512);
     static constexpr int kQRows = kPair ? 128 : TQ;                                 // Q rows this CTA holds of a tile
@@ -84,7 +89,8 @@ struct __align__(8) LinCtl {
     uint64_t full[kLinMaxStages];      // operands landed and scales in tensor memory
     uint64_t empty[kLinMaxStages];     // the stage's MMAs are done
     uint64_t sf_full[kLinMaxStages];   // scale tiles landed in shared memory
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t acc_full[2], acc_empty[2];   // accumulator: a tile's sums are there / all read
+    uint64_t acc_part[2];                 // its columns that the other accumulator shares are read
     uint32_t tmem;
     volatile int abort;
     volatile int issued[2];           // stages issued by each producer
@@ -94,8 +100,7 @@ struct __align__(8) LinCtl {
 template <int TQ>
 constexpr size_t LinCfg<TQ>::ctl_bytes() { return oCtl + sizeof(LinCtl) + 1024; }
 
-// (inlined: a call would keep the register split below from being allocated)
-__device__ __forceinline__ void lin_report(const LinParams& p, int role, long long parity) {
+__device__ __noinline__ void lin_report(const LinParams& p, int role, long long parity) {
     DevStatus* st = p.status;
     const unsigned long long mine = (p.launch_id << 8) | (unsigned long long)kErrTimeout;
     unsigned long long cur = atomicAdd(&st->key, 0ull);
@@ -120,17 +125,18 @@ template <bool kCluster = false>
 __device__ __forceinline__ bool lin_try(uint64_t* bar, uint32_t parity) {
     return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
 }
+// False once the CTA gave up.
 template <bool kCluster = false>
-__device__ __forceinline__ void lin_wait(const LinParams& p, LinCtl* ctl, uint64_t* bar, uint32_t parity, int role) {
-    if (lin_try<kCluster>(bar, parity)) return;
+__device__ __forceinline__ bool lin_wait(const LinParams& p, LinCtl* ctl, uint64_t* bar, uint32_t parity, int role) {
+    if (lin_try<kCluster>(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
-        if (lin_try<kCluster>(bar, parity)) return;
-        if (ctl->abort) return;
+        if (lin_try<kCluster>(bar, parity)) return true;
+        if (ctl->abort) return false;
         if ((n & 63) == 0 && globaltimer() - t0 > (uint64_t)p.timeout_ns) {
             lin_report(p, role, (long long)parity);
             ctl->abort = 1;
-            return;
+            return false;
         }
     }
 }
@@ -138,18 +144,17 @@ __device__ __forceinline__ void lin_wait(const LinParams& p, LinCtl* ctl, uint64
 struct LinItem {
     int group;
     int p0;              // this CTA's first P row inside the group
-    long long q0;        // first Q row
+    int q0;              // first Q row
     int nq;              // Q rows multiplied: up to the segment's end, a multiple of 32
-    long long q_end;     // Q rows past this are not this tile's (segment end)
-    long long q_live;    // Q rows past this are padding: zeros are written
+    int q_end;           // Q rows past this are not this tile's (segment end)
+    int q_live;          // Q rows past this are padding: zeros are written
     int b0, b1;          // 32-blocks of the contraction
     int kb0, kb1;        // 128-blocks this CTA reads
 };
 
-__device__ __forceinline__ int seg_start(const LinParams& p, int g, long long limit) {
+__device__ __forceinline__ int seg_start(const LinParams& p, int g, int limit) {
     // 32-row granular and inside the buffers, whatever the array holds
-    const long long o = __ldg(p.offsets + g);
-    return (int)(max(0ll, min(o, limit)) & ~31ll);
+    return max(0, min(__ldg(p.offsets + g), limit)) & ~31;
 }
 
 template <int TQ>
@@ -162,13 +167,13 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
         const int r = tile - it.group * per;
         q_tile = r / p.pt;
         p_tile = r - q_tile * p.pt;
-        it.q0 = (long long)q_tile * TQ;
+        it.q0 = q_tile * TQ;
         it.q_end = it.q_live = p.q_rows;
         it.b0 = 0;
         it.b1 = p.blocks;
         if (p.offsets) {
-            it.b0 = seg_start(p, it.group, (long long)p.blocks * 32) / 32;
-            it.b1 = max(it.b0, seg_start(p, it.group + 1, (long long)p.blocks * 32) / 32);
+            it.b0 = seg_start(p, it.group, p.blocks * 32) / 32;
+            it.b1 = max(it.b0, seg_start(p, it.group + 1, p.blocks * 32) / 32);
         }
     } else {
         int lo = 0, hi = p.groups - 1;   // the last group that starts at or before this tile
@@ -185,21 +190,19 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
         const int band = r / (kBand * qt), np = min(kBand, p.pt - band * kBand), rb = r - band * kBand * qt;
         q_tile = rb / np;
         p_tile = band * kBand + rb - q_tile * np;
-        long long o = 0;
+        int o = 0;
         it.q_end = it.q_live = p.q_rows;
         if (p.offsets) {
             o = seg_start(p, lo, p.q_rows);
-            it.q_end = lo + 1 == p.groups ? min((long long)__ldg(p.offsets + lo + 1), (long long)p.q_rows)
-                                          : (long long)seg_start(p, lo + 1, p.q_rows);
-            it.q_live = min(it.q_end, o + max(0, __ldg(p.counts + lo)));
+            it.q_end = lo + 1 == p.groups ? min(__ldg(p.offsets + lo + 1), p.q_rows) : seg_start(p, lo + 1, p.q_rows);
+            it.q_live = o + min(max(0, it.q_end - o), max(0, __ldg(p.counts + lo)));
         }
-        it.q0 = o + (long long)q_tile * TQ;
+        it.q0 = o + q_tile * TQ;
         it.b0 = 0;
         it.b1 = p.blocks;
     }
     it.p0 = p_tile * (LinCfg<TQ>::kPair ? 256 : 128) + (LinCfg<TQ>::kPair ? rank * 128 : 0);
-    it.nq = (int)min((long long)TQ, (it.q_end - it.q0 + 31) & ~31ll);
-    if (it.nq < 32) it.nq = 32;   // (a tile past its segment's end, which only foreign offsets make: nothing is stored)
+    it.nq = max(32, min(TQ, (it.q_end - it.q0 + 31) & ~31));   // (a tile past its segment's end, which only foreign offsets make: nothing is stored)
     const int lo = it.b0 / 4, hi = it.b1 > it.b0 ? (it.b1 + 3) / 4 : lo;
     if (LinCfg<TQ>::kPair) {
         it.kb0 = lo;
@@ -223,10 +226,10 @@ struct LinShare {
 };
 __device__ __forceinline__ LinShare lin_share(const LinParams& p, const LinItem& it, int f, int col0) {
     LinShare e;
-    const long long q = it.q0 + col0;
+    const int q = it.q0 + col0;
     e.row = (p.by_contraction ? (long long)it.group * p.q_rows : 0) + q;
-    e.end = (int)max(0ll, it.q_end - q);
-    e.live = (int)max(0ll, min(it.q_live - q, (long long)e.end));
+    e.end = max(0, it.q_end - q);
+    e.live = max(0, min(it.q_live - q, e.end));
     e.f = f;
     e.bias = p.bias && f < p.p_rows ? __ldg(p.bias + (size_t)it.group * p.p_rows + f) : 0.f;
     return e;
@@ -347,14 +350,6 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
     }
 }
 
-// columns of a warp's share that the pair kernel's epilogue finishes before it
-// releases the accumulator (the others wait in registers)
-constexpr int kDirectCols = 32;
-// registers: the pair kernel's epilogue keeps 96 columns of the accumulator; 8 warps x 168 + 8 x 88 are the launch's 16 x 128
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 // arrive on a barrier of another CTA without ordering earlier memory accesses (a
 // release waits for every earlier global store, about 1 us; what the barrier
 // hands over is tensor memory, whose accesses are complete: tcgen05.wait::st / ::ld)
@@ -387,6 +382,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->acc_full[b], 1);
             mbar_init(&ctl->acc_empty[b], kPair ? 2 * C::kEpiWarps : C::kEpiWarps);
+            mbar_init(&ctl->acc_part[b], C::kEpiWarps);   // (half of either CTA's epilogue warps)
         }
         ctl->abort = 0;
         ctl->issued[0] = ctl->issued[1] = 0;
@@ -413,13 +409,13 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 const int g = g0 + lane;
                 int n = 0;
                 if (g < p.groups) {
-                    long long len = p.q_rows;
+                    int len = p.q_rows;
                     if (p.offsets) {
                         const int lo = seg_start(p, g, p.q_rows);
-                        const long long hi = min((long long)__ldg(p.offsets + g + 1), (long long)p.q_rows);
-                        len = max(0ll, hi - lo);
+                        const int hi = min(__ldg(p.offsets + g + 1), p.q_rows);
+                        len = max(0, hi - lo);
                     }
-                    n = (int)((len + TQ - 1) / TQ) * p.pt;
+                    n = (len + TQ - 1) / TQ * p.pt;
                 }
                 int inc = n;
 #pragma unroll
@@ -443,9 +439,6 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 
     if (kPair || split) cluster_sync();   // every CTA of the cluster runs before any touches its shared memory
 
-    // (whole warpgroups take each side; each side's code follows its register count)
-    if (warp < 8) {
-    if constexpr (kPair) regs_down<88>();
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------- TMA producers
         const int pid = warp / 2;
@@ -456,8 +449,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         const uint64_t keep = l2_policy_evict_last();
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
-            const int qa = (int)(it.q0 >> 7);                                   // first scale tile of the Q rows
-            const int atoms = min((int)((it.q0 & 127) + TQ + 127) >> 7, p.q_row_tiles - qa);
+            const int qa = it.q0 >> 7;                                          // first scale tile of the Q rows
+            const int atoms = min(((it.q0 & 127) + TQ + 127) >> 7, p.q_row_tiles - qa);
             const int pa = min(it.p0 >> 7, p.p_row_tiles - 1);                  // (a pair's second half may lie past P)
             const int py = (p.by_contraction ? 0 : it.group * p.p_rows) + it.p0;
             const int half = it.nq / 2, boxes = (half + 31) / 32;               // pair: Q rows of each CTA, in boxes of 32
@@ -465,8 +458,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                     if ((n & 1) != pid) continue;
                     const int stage = n % C::kStages;
-                    lin_wait<kPair>(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma);
-                    if (ctl->abort) break;
+                    if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma)) break;
                     mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
                     bulk_load(smem + C::oSfp + stage * 512,
                               p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
@@ -482,7 +474,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                         const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
                         if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
                         tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
-                        const int qy = (int)it.q0 + rank * half;
+                        const int qy = it.q0 + rank * half;
                         if (whole)
                             tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
                         else
@@ -491,7 +483,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     } else {
                         mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
                         tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
-                        tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, (int)it.q0);
+                        tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, it.q0);
                     }
                     ctl->issued[pid] = n + 1;
                 }
@@ -504,41 +496,53 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer (pair: the even CTA's, for both)
+        // Its time from one stage to the next is what bounds the product (every
+        // instruction here counts once per stage): one wait, no other shared-memory
+        // access, the descriptors by addition.
         const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | (1u << 23) | ((kPair ? 16u : 8u) << 24);
-        int n = 0, acc = 0;
+        const uint64_t ad0 = smem_desc(smem_u32(smem + C::oP), 16, 1024, kLayoutSw128);
+        const uint64_t bd0 = smem_desc(smem_u32(smem + C::oQ), 16, 1024, kLayoutSw128);
+        int stage = 0, acc = 0;
+        uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             if (lane == 0 && it.kb1 > it.kb0) {
-                const int buf = acc % C::kAccBufs;
-                lin_wait<kPair>(p, ctl, &ctl->acc_empty[buf], ((acc / C::kAccBufs) & 1) ^ 1, kRoleMma);
+                const int buf = acc & 1;
+                lin_wait<kPair>(p, ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
+                if (C::kOverlap && acc) lin_wait<kPair>(p, ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * TQ);
+                const uint32_t d = tmem + (uint32_t)(buf * C::kAccStep);
                 const uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
                 uint32_t some = 0;
-                for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                    const int stage = n % C::kStages;
-                    const uint32_t ph = (n / C::kStages) & 1;
-                    lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma);
-                    if (ctl->abort) break;
+                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                    if (!lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
-                    const uint64_t ad = smem_desc(smem_u32(smem + C::oP + (size_t)stage * kAStageBytes), 16, 1024, kLayoutSw128);
-                    const uint64_t bd = smem_desc(smem_u32(smem + C::oQ + (size_t)stage * C::kQBytes), 16, 1024, kLayoutSw128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (kb * 4 + k < it.b0 || kb * 4 + k >= it.b1) continue;
+                    const uint64_t ad = ad0 + (uint32_t)(stage * (kAStageBytes >> 4));
+                    const uint64_t bd = bd0 + (uint32_t)(stage * (C::kQBytes >> 4));
+                    auto step = [&](int k) {   // 32 of the contraction: +32 bytes inside the swizzled 128, scale byte k
                         const uint32_t idesc = idesc1 | ((uint32_t)k << 4) | ((uint32_t)k << 29);
                         if constexpr (kPair)
                             mma_mxf8f6f4_pair(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
                         else
                             mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
                         some = 1;
+                    };
+                    if (kb * 4 >= it.b0 && kb * 4 + 4 <= it.b1) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) step(k);
+                    } else {   // a range that starts or ends inside the block
+                        for (int k = max(0, it.b0 - kb * 4); k < min(4, it.b1 - kb * 4); ++k) step(k);
                     }
                     if constexpr (kPair)
                         tc_commit_pair_multicast(&ctl->empty[stage], 0x3);
                     else
                         tc_commit(&ctl->empty[stage]);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        ph ^= 1;
+                    }
                 }
                 if constexpr (kPair)
                     tc_commit_pair_multicast(&ctl->acc_full[buf], 0x3);
@@ -559,7 +563,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         int n = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
-            const int shift = (int)(it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
+            const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 const int stage = n % C::kStages;
                 lin_wait(p, ctl, &ctl->sf_full[stage], (n / C::kStages) & 1, kRoleScale);
@@ -600,72 +604,74 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 cluster_sync();
             }
         }
-    } else if (split) {
-        for (int tile = first; tile < total; tile += stride) {
-            cluster_sync();
-            cluster_sync();
-        }
-    }
-    } else {
+    } else if (warp >= 8) {
         // ---------------------------------------------------------- epilogue
-        if constexpr (kPair) regs_up<168>();
         const int quarter = warp & 3, part = (warp - 8) >> 2;
         float* partial = reinterpret_cast<float*>(smem);   // [TQ][128]: the split tiles' (over the stages)
         int acc = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             const bool live = it.kb1 > it.kb0;
-            const int buf = acc % C::kAccBufs;
+            const int buf = acc & 1;
             const int f = it.p0 + quarter * 32 + lane;
             const bool in_p = it.p0 + quarter * 32 < p.p_rows;   // (P rows come in blocks of 32: uniform over the warp)
-            const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * TQ + part * C::kColsPerWarp);
+            const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kAccStep + part * C::kColsPerWarp);
             if (live) {
-                lin_wait<kPair>(p, ctl, &ctl->acc_full[buf], (acc / C::kAccBufs) & 1, kRoleEpi);
+                lin_wait<kPair>(p, ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
                 __syncwarp();
                 tc_fence_after();
             }
             const LinShare e = lin_share(p, it, f, part * C::kColsPerWarp);
             if constexpr (kPair) {
-                // The first columns straight from the accumulator, the rest into
-                // registers, the accumulator released, then 32 columns at a time
-                // (the rest moves down: one copy of the code).
-                constexpr int kHeld = C::kColsPerWarp - kDirectCols;
-                float v[kHeld];
+                // The 64 columns that the next tile's accumulator takes over (the
+                // tile's last in the first accumulator, its first in the second)
+                // go to registers first and are handed over; 32 columns at a time
+                // then come from there or from tensor memory.
+                const int over = buf == 0 ? C::kColsPerWarp - C::kOverlap : 0;
+                const bool mine = live && part == (buf ^ 1);
+                float v[C::kOverlap];
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < C::kOverlap; i += 32)
+                        tmem_ld_32x32b_x32(t + (uint32_t)(over + i), *reinterpret_cast<uint32_t(*)[32]>(v + i));
+                    tc_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive(&ctl->acc_part[buf]);
+                        else
+                            mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&ctl->acc_part[buf]), 0));
+                    }
+                }
 #pragma unroll 1
                 for (int c = 0; c < C::kColsPerWarp; c += 32) {
                     float u[32];
-                    if (c < kDirectCols) {
-                        if (live) {
-                            tmem_ld_32x32b_x32(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(u));
-                            tc_wait_ld();
-                        }
-                    } else {
-                        if (c == kDirectCols && live) {
-#pragma unroll
-                            for (int i = 0; i < kHeld; i += 32)
-                                tmem_ld_32x32b_x32(t + (uint32_t)(kDirectCols + i), *reinterpret_cast<uint32_t(*)[32]>(v + i));
-                            tc_wait_ld();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (rank == 0)
-                                    mbar_arrive(&ctl->acc_empty[buf]);
-                                else
-                                    mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&ctl->acc_empty[buf]), 0));
-                            }
-                        }
+                    if (mine && c >= over && c < over + C::kOverlap) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) u[j] = v[j];
 #pragma unroll
-                        for (int j = 0; j < kHeld - 32; ++j) v[j] = v[j + 32];
-                    }
-                    if (!live) {
+                        for (int j = 0; j < C::kOverlap - 32; ++j) v[j] = v[j + 32];
+                    } else if (live) {
+                        tmem_ld_32x32b_x32(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(u));
+                        tc_wait_ld();
+                    } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) u[j] = 0.f;
                     }
                     if (in_p) lin_store<32>(p, e, c, lane, u);
                 }
-                if (live) ++acc;
+                if (live) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive(&ctl->acc_empty[buf]);
+                        else
+                            mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&ctl->acc_empty[buf]), 0));
+                    }
+                    ++acc;
+                }
             } else {
 #pragma unroll 1
                 for (int c = 0; c < C::kColsPerWarp; c += 16) {
@@ -713,6 +719,11 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     cluster_sync();   // the partial tiles have been read: the stages may be filled again
                 }
             }
+        }
+    } else if (split) {
+        for (int tile = first; tile < total; tile += stride) {
+            cluster_sync();
+            cluster_sync();
         }
     }
     __syncthreads();
