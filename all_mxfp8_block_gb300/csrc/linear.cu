@@ -278,13 +278,13 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
     // (0 stays 0 on padding rows)
     if (p.act == kActGelu) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActGelu);
+        for (int j = 0; j < NC; ++j) v[j] = act_value<kActGelu>(v[j]);
     } else if (p.act == kActSilu) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActSilu);
+        for (int j = 0; j < NC; ++j) v[j] = act_value<kActSilu>(v[j]);
     } else if (p.act == kActRelu) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) v[j] = act_value(v[j], kActRelu);
+        for (int j = 0; j < NC; ++j) v[j] = act_value<kActRelu>(v[j]);
     }
     if (p.residual) {
         const int odd = lane & 1, left = e.live - j0 - odd;

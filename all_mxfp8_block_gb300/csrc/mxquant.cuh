@@ -117,42 +117,59 @@ __device__ __forceinline__ size_t scale_word(int kb, long long r, int rt) {
     return ((size_t)kb * rt + (size_t)(r >> 7)) * 512 + (size_t)((r & 31) * 16 + ((r & 127) >> 5) * 4);
 }
 
-// activations and their derivatives in fp32 (ids as in the C ABI).  tanh and
-// the logistic function through exp of a non-positive argument: no overflow,
-// and a relative error of a few fp32 roundings.
-constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
-// s = logistic(x), c = 1 - s, each to a few roundings of its own size
-__device__ __forceinline__ void logistic(float x, float& s, float& c) {
-    const float t = __expf(-fabsf(x));
-    const float h = __fdividef(1.f, 1.f + t), l = t * h;
-    s = x >= 0.f ? h : l;
-    c = x >= 0.f ? l : h;
-    if (x != x) s = c = x;
+__device__ __forceinline__ float exp2f_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-constexpr float kGeluA = 0.7978845608028654f, kGeluB = 0.044715f;   // sqrt(2 / pi)
-// 0.5 (1 + tanh u) = logistic(2 u)
-__device__ __forceinline__ float act_value(float z, int act) {
-    float s, c;
-    if (act == kActRelu) return z > 0.f || z != z ? z : 0.f;
-    if (act == kActGelu) {
-        logistic(2.f * kGeluA * (z + kGeluB * z * z * z), s, c);
-        return z * s;
-    }
-    if (act == kActSilu) {
-        logistic(z, s, c);
-        return z * s;
+// maxima and minima that keep a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Activations and their derivatives in fp32 (ids as in the C ABI), through
+// s = logistic(x) = 1 / (1 + e), e = exp(-x), and 1 - s = s e: each to a few
+// roundings of its own size (ex2 and reciprocal approximations of 2^-22).
+//   gelu(z) = 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
+// The logistic's argument is kept where e is finite, i.e. z >= -87 (silu) or
+// |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35.
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluA = 2.f * 0.7978845608028654f, kGeluB = 0.044715f;   // 2 sqrt(2 / pi)
+__device__ __forceinline__ float logistic_e(float e) { return __fdividef(1.f, 1.f + e); }
+template <int kAct>
+__device__ __forceinline__ float act_value(float z) {
+    if constexpr (kAct == kActRelu) {
+        return max_nan(z, 0.f);
+    } else if constexpr (kAct == kActSilu) {
+        const float l = max_nan(z, -87.f);
+        return l * logistic_e(exp2f_approx(-kLog2e * l));
+    } else if constexpr (kAct == kActGelu) {
+        const float l = max_nan(z, -10.f), m = min_nan(l, 10.f);
+        const float u = m * fmaf(kGeluA * kGeluB * -kLog2e, m * m, kGeluA * -kLog2e);
+        return l * logistic_e(exp2f_approx(u));
     }
     return z;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-    float s, c;
-    if (act == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-    if (act == kActGelu || act == kActSilu) {
-        const bool g = act == kActGelu;
-        logistic(g ? 2.f * kGeluA * (z + kGeluB * z * z * z) : z, s, c);
-        const float t = s * c;
-        if (t == 0.f) return s;   // saturated: z's own size (it may be infinite) no longer matters
-        return s + z * t * (g ? 2.f * kGeluA * (1.f + 3.f * kGeluB * z * z) : 1.f);
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+    if constexpr (kAct == kActRelu) {
+        return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    } else if constexpr (kAct == kActSilu) {
+        const float m = min_nan(max_nan(z, -87.f), 87.f);
+        const float e = exp2f_approx(-kLog2e * m), s = logistic_e(e);
+        return fmaf(m * s, s * e, s);
+    } else if constexpr (kAct == kActGelu) {
+        const float m = min_nan(max_nan(z, -10.f), 10.f), m2 = m * m;
+        const float e = exp2f_approx(m * fmaf(kGeluA * kGeluB * -kLog2e, m2, kGeluA * -kLog2e)), s = logistic_e(e);
+        return fmaf(m * s * (s * e), fmaf(3.f * kGeluA * kGeluB, m2, kGeluA), s);
     }
     return 1.f;
 }

@@ -469,7 +469,7 @@ int mxa2a_linear_backward(mxa2a_linear* l, int64_t rows, const void* dy, const v
     q.seg = seg;
     if (dbias) q.colsum = l->colsum;
     if (launch_quantize(q, st) != cudaSuccess) return MXA2A_ERR_CUDA;
-    l->launches += 1 + (q.scale_t && l->N % 128 ? 1 : 0);
+    ++l->launches;
     if (dbias) {
         if (launch_bias_sums(l->colsum, seg, l->N, static_cast<float*>(dbias), st) != cudaSuccess) return MXA2A_ERR_CUDA;
         ++l->launches;

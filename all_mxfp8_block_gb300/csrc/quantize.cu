@@ -10,16 +10,16 @@ namespace mxa2a {
 
 namespace {
 
-// A CTA takes a tile of kTileRows x kTileCols elements, read once.  Thread
-// (ty, tx) holds 8 consecutive columns of kPass rows: a row's 32-column block
-// is 4 threads, its largest value two shuffles.  For the transposed
-// quantisation the tile goes through shared memory (rows kTileCols + 1 words
-// apart: no bank conflicts either way), and a thread takes one column's 32
-// rows.  Bound by the bytes read and written; the tile's codes leave in
-// 32-byte pieces (64-byte rows one way, 32 rows' bytes the other).
+// A CTA takes a tile of 128 rows x 64 columns, read once.  Thread (ty, tx) holds
+// 8 consecutive columns of the rows ty, ty + 32, ...: a row's 32-column block is
+// 4 threads, its largest value two shuffles.  For the transposed quantisation
+// the tile goes through shared memory in 16-byte accesses; a thread then takes
+// 8 rows of 4 columns, 4 threads (8 lanes apart) a column's 32 rows.  The bytes
+// bound it on paper; measured, instructions do (each element is scaled,
+// converted and compared twice, and the activation's slope costs a dozen), so
+// the activation is a template argument and maxima are single instructions.
 constexpr int kTileRows = 128, kTileCols = 64, kQThreads = 256;
 constexpr int kPass = kTileRows * kTileCols / (kQThreads * 8);
-constexpr int kLd = kTileCols + 1;
 
 // segment of row r (offsets ascending), and whether r holds a token of it
 __device__ __forceinline__ bool row_is_token(const Segments& s, long long r) {
@@ -32,15 +32,18 @@ __device__ __forceinline__ bool row_is_token(const Segments& s, long long r) {
     return r >= o && r < o + __ldg(s.counts + lo);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(Quantize q, int row_tiles) {
-    __shared__ float tile[kTileRows * kLd];
+__device__ __forceinline__ float abs_max(float m, float v) { return max_nan(m, fabsf(v)); }
+
+template <typename T, int kAct>
+__global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int row_tiles) {
+    __shared__ float4 tile[kTileRows * (kTileCols / 4)];
     __shared__ uint8_t token[kTileRows];
     const int g = (int)(blockIdx.x / row_tiles);
     const long long r0 = (long long)(blockIdx.x % row_tiles) * kTileRows;
     const int c0 = (int)blockIdx.y * kTileCols;
     const int tx = threadIdx.x % (kTileCols / 8), ty = threadIdx.x / (kTileCols / 8);
-    const int emax = mx_emax(q.e5m2);
+    const bool e5m2 = q.e5m2;
+    const int emax = mx_emax(e5m2);
     const bool masked = q.seg.offsets != nullptr;
     if (masked) {
         if (r0 >= __ldg(q.seg.offsets + q.seg.experts)) return;   // past the last segment: nothing is read from there
@@ -49,25 +52,36 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(Quantize q, int row
         __syncthreads();
     }
     const T* x = static_cast<const T*>(q.x) + (long long)g * q.rows * q.ldx;
-    const int rt = (int)((q.rows + 127) / 128), kb = (c0 + tx * 8) >> 7;
+    const int rt = (int)((q.rows + 127) / 128), kb = c0 >> 7;
     const int col = c0 + tx * 8;
     const bool in_cols = col < q.cols;   // (columns come in blocks of 32)
     float v[kPass][8];
+    bool live[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-        const long long r = r0 + ty + p * (kTileRows / kPass);
-        const bool live = in_cols && r < q.rows && (!masked || token[r - r0]);
-        if (live) {
+        const int i = ty + p * 32;
+        const long long r = r0 + i;
+        live[p] = in_cols && r < q.rows && (!masked || token[i]);
+        if (live[p]) {
             Vec<T, 8>::load(x + r * q.ldx + col, v[p]);
-            if (q.preact) {
-                float z[8];
-                Vec<__nv_bfloat16, 8>::load(static_cast<const __nv_bfloat16*>(q.preact) + r * q.cols + col, z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] *= act_slope(z[i], q.act);
-            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+            for (int j = 0; j < 8; ++j) v[p][j] = 0.f;
+        }
+    }
+    if constexpr (kAct != kActNone) {
+        uint4 zw[kPass];
+#pragma unroll
+        for (int p = 0; p < kPass; ++p)
+            zw[p] = live[p] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.preact) +
+                                                                   (r0 + ty + p * 32) * q.cols + col))
+                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int p = 0; p < kPass; ++p) {
+            float z[8];
+            Vec<__nv_bfloat16, 8>::unpack(&zw[p], z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[p][j] *= act_slope<kAct>(z[j]);
         }
     }
     if (q.codes) {
@@ -75,89 +89,107 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(Quantize q, int row
         uint8_t* scale = q.scale + (size_t)g * ((q.cols + 127) / 128) * rt * 512;
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
-            const long long r = r0 + ty + p * (kTileRows / kPass);
-            uint32_t m = 0;
+            const long long r = r0 + ty + p * 32;
+            float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[p][i]) & 0x7fffffffu);
-            m = max(m, __shfl_xor_sync(kLanes, m, 1));
-            m = max(m, __shfl_xor_sync(kLanes, m, 2));
-            const uint32_t byte = mx_scale_byte(m, emax);
+            for (int j = 0; j < 8; ++j) m = abs_max(m, v[p][j]);
+            m = max_nan(m, __shfl_xor_sync(kLanes, m, 1));
+            m = max_nan(m, __shfl_xor_sync(kLanes, m, 2));
+            const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
             const float inv = mx_inv_scale(byte);
-            const uint2 w = make_uint2(mx_codes4(v[p], inv, byte == 255, q.e5m2), mx_codes4(v[p] + 4, inv, byte == 255, q.e5m2));
+            const uint2 w = make_uint2(mx_codes4(v[p], inv, byte == 255, e5m2), mx_codes4(v[p] + 4, inv, byte == 255, e5m2));
             if (in_cols && r < q.rows) *reinterpret_cast<uint2*>(codes + r * q.cols + col) = w;
             // two blocks of the tile's row in one 16-bit store (a tile is half a scale word wide)
             const uint32_t other = __shfl_xor_sync(kLanes, byte, 4);
-            if (tx == 0)   // (rows past the last get scale 0, so that every byte of a tile is written)
-                *reinterpret_cast<uint16_t*>(scale + scale_word(kb, r, rt) + ((c0 >> 5) & 3)) =
-                    (uint16_t)(byte | (c0 + 32 < q.cols ? other : 0u) << 8);
-            // the last tile of columns also clears the word's bytes past the last column
-            if (tx == 0 && c0 + kTileCols >= q.cols && (c0 & 64) == 0)
-                *reinterpret_cast<uint16_t*>(scale + scale_word(kb, r, rt) + 2) = 0;
+            if (tx == 0) {   // (rows past the last and blocks past the last column get scale 0: every byte is written)
+                uint16_t* s = reinterpret_cast<uint16_t*>(scale + scale_word(kb, r, rt) + ((c0 >> 5) & 3));
+                s[0] = (uint16_t)(byte | (c0 + 32 < q.cols ? other : 0u) << 8);
+                if (c0 + kTileCols >= q.cols && (c0 & 64) == 0) s[1] = 0;
+            }
         }
     }
     if (!q.codes_t && !q.colsum) return;
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-        float* t = tile + (ty + p * (kTileRows / kPass)) * kLd + tx * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = v[p][i];
+        // (the upper four threads of a row swap the order of their halves: no bank conflicts)
+        float4* t = tile + (ty + p * 32) * (kTileCols / 4) + tx * 2;
+        const float4 lo = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]), hi = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
+        const int swap = tx >> 2;
+        t[swap] = swap ? hi : lo;
+        t[swap ^ 1] = swap ? lo : hi;
     }
     __syncthreads();
-    // one column's 32 rows
-    const int c = threadIdx.x % kTileCols, rb = threadIdx.x / kTileCols;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int c4 = (lane & 7) + 8 * (warp & 1), rg = lane >> 3, rb = warp >> 1;   // 4 columns; 8 of the 32 rows of block rb
     const long long t0 = r0 + rb * 32;
-    if (c0 + c >= q.cols) return;
-    float u[32];
-    uint32_t m = 0;
-    float sum = 0.f;
+    const int ct = (int)((q.cols + 127) / 128), c = c0 + c4 * 4;
+    const bool in_c = c < q.cols;
+    float u[8][4], m[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        u[i] = tile[(rb * 32 + i) * kLd + c];
-        m = max(m, __float_as_uint(u[i]) & 0x7fffffffu);
-        sum += u[i];
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = tile[(rb * 32 + rg * 8 + i) * (kTileCols / 4) + c4];
+        u[i][0] = f.x;
+        u[i][1] = f.y;
+        u[i][2] = f.z;
+        u[i][3] = f.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = abs_max(m[j], u[i][j]);
+            sum[j] += u[i][j];
+        }
     }
-    if (q.colsum && t0 < q.rows) q.colsum[(t0 >> 5) * q.cols + c0 + c] = sum;
+    if (q.colsum) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum[j] += __shfl_xor_sync(kLanes, sum[j], 8);
+            sum[j] += __shfl_xor_sync(kLanes, sum[j], 16);
+        }
+        if (rg == 0 && in_c && t0 < q.rows)
+            *reinterpret_cast<float4*>(q.colsum + (t0 >> 5) * q.cols + c) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    }
     if (!q.codes_t) return;
     const long long ld_t = (q.rows + 31) / 32 * 32;
-    const int ct = (int)((q.cols + 127) / 128);
-    const uint32_t byte = mx_scale_byte(m, emax);
-    const float inv = mx_inv_scale(byte);
-    if (t0 < ld_t) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = mx_codes4(u + 4 * i, inv, byte == 255, q.e5m2);
-        uint4* o = reinterpret_cast<uint4*>(q.codes_t + ((long long)g * q.cols + c0 + c) * ld_t + t0);
-        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
     uint8_t* scale_t = q.scale_t + (size_t)g * rt * ct * 512;
-    scale_t[scale_word((int)(r0 >> 7), c0 + c, ct) + rb] = t0 < ld_t ? (uint8_t)byte : 0;
-}
-
-// Columns of the last scale tile past the last column (transposed output):
-// their bytes are cleared so that a tile never holds stale bytes.
-__global__ void clear_tail_kernel(uint8_t* scale_t, int groups, int rt, int ct, int cols) {
-    const int tail = ct * 128 - cols;
-    const long long n = (long long)groups * rt * tail;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
-        const int c = cols + (int)(i % tail);
-        const long long k = i / tail;   // group * rt + row tile
-        *reinterpret_cast<uint32_t*>(scale_t + (size_t)(k / rt) * rt * ct * 512 + scale_word((int)(k % rt), c, ct)) = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[j] = max_nan(m[j], __shfl_xor_sync(kLanes, m[j], 8));
+        m[j] = max_nan(m[j], __shfl_xor_sync(kLanes, m[j], 16));
+        const uint32_t byte = mx_scale_byte(__float_as_uint(m[j]), emax);
+        const float inv = mx_inv_scale(byte);
+        const float a[4] = {u[0][j], u[1][j], u[2][j], u[3][j]}, b[4] = {u[4][j], u[5][j], u[6][j], u[7][j]};
+        if (in_c && t0 < ld_t)
+            *reinterpret_cast<uint2*>(q.codes_t + ((long long)g * q.cols + c + j) * ld_t + t0 + rg * 8) =
+                make_uint2(mx_codes4(a, inv, byte == 255, e5m2), mx_codes4(b, inv, byte == 255, e5m2));
+        if (in_c && rg == 0) scale_t[scale_word((int)(r0 >> 7), c + j, ct) + rb] = t0 < ld_t ? (uint8_t)byte : 0;
     }
+    // the words of the last scale tile past the last column
+    if (c0 + kTileCols >= q.cols)
+        for (int i = (int)q.cols + threadIdx.x; i < ct * 128; i += kQThreads)
+            *reinterpret_cast<uint32_t*>(scale_t + scale_word((int)(r0 >> 7), i, ct)) = 0;
 }
 
-__global__ void bias_sums_kernel(const float* colsum, Segments s, long long cols, float* dbias) {
-    const long long c = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const int g = blockIdx.y;
-    if (c >= cols) return;
+// dbias: the 32-row blocks' column sums of a segment, added in order: a CTA
+// takes 32 columns of a group, its 8 warps an eighth of the blocks each.
+__global__ void __launch_bounds__(256) bias_sums_kernel(const float* colsum, Segments s, long long cols, float* dbias) {
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = blockIdx.y;
+    const long long c = (long long)blockIdx.x * 32 + lane;   // (columns come in blocks of 32)
     long long lo = 0, hi = (s.rows + 31) / 32;
     if (s.offsets) {
         lo = max(0, __ldg(s.offsets + g)) / 32;
         hi = min(hi, (long long)__ldg(s.offsets + g + 1) / 32);
     }
+    const long long per = (max(0ll, hi - lo) + 7) / 8, b1 = min(hi, lo + (warp + 1) * per);
     float sum = 0.f;
-    for (long long b = lo; b < hi; ++b) sum += __ldg(colsum + b * cols + c);
-    dbias[(long long)g * cols + c] = sum;
+#pragma unroll 8
+    for (long long b = lo + warp * per; b < b1; ++b) sum += __ldg(colsum + b * cols + c);
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        sum = 0.f;
+        for (int w = 0; w < 8; ++w) sum += part[w][lane];
+        dbias[(long long)g * cols + c] = sum;
+    }
 }
 
 __global__ void scale_tiles_kernel(const uint8_t* s, int groups, long long rows, long long blocks, uint32_t* tiles, int rt, int bt) {
@@ -177,23 +209,25 @@ __global__ void scale_tiles_kernel(const uint8_t* s, int groups, long long rows,
 
 cudaError_t launch_quantize(const Quantize& q, cudaStream_t stream) {
     const int row_tiles = (int)((q.rows + kTileRows - 1) / kTileRows);
-    const int ct = (int)((q.cols + 127) / 128);
     const dim3 grid((unsigned)((long long)row_tiles * q.groups), (unsigned)((q.cols + kTileCols - 1) / kTileCols));
-    if (q.x_type == kTypeBf16)
-        quantize_kernel<__nv_bfloat16><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else if (q.x_type == kTypeF16)
-        quantize_kernel<__half><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
+    if (q.x_type == kTypeF16)
+        quantize_kernel<__half, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
+    else if (q.x_type == kTypeF32)
+        quantize_kernel<float, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
+    else if (!q.preact)
+        quantize_kernel<__nv_bfloat16, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
+    else if (q.act == kActRelu)
+        quantize_kernel<__nv_bfloat16, kActRelu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
+    else if (q.act == kActGelu)
+        quantize_kernel<__nv_bfloat16, kActGelu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
     else
-        quantize_kernel<float><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    if (q.scale_t && q.cols % 128)
-        clear_tail_kernel<<<std::min<long long>(1024, (long long)q.groups * row_tiles), 128, 0, stream>>>(
-            q.scale_t, q.groups, row_tiles, ct, (int)q.cols);
+        quantize_kernel<__nv_bfloat16, kActSilu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
     return cudaGetLastError();
 }
 
 cudaError_t launch_bias_sums(const float* colsum, const Segments& seg, long long cols, float* dbias, cudaStream_t stream) {
-    const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)seg.experts);
-    bias_sums_kernel<<<grid, 128, 0, stream>>>(colsum, seg, cols, dbias);
+    const dim3 grid((unsigned)(cols / 32), (unsigned)seg.experts);
+    bias_sums_kernel<<<grid, 256, 0, stream>>>(colsum, seg, cols, dbias);
     return cudaGetLastError();
 }
 
