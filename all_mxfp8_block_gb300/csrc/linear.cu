@@ -29,6 +29,7 @@
 // output is then undefined) and the status block tells.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "linear.cuh"
 #include "mxquant.cuh"
 #include "ptx.cuh"
@@ -154,7 +155,7 @@ struct LinItem {
 
 __device__ __forceinline__ int seg_start(const LinParams& p, int g, int limit) {
     // 32-row granular and inside the buffers, whatever the array holds
-    return max(0, min(__ldg(p.offsets + g), limit)) & ~31;
+    return max(0, min(*(p.offsets + g), limit)) & ~31;
 }
 
 template <int TQ>
@@ -194,8 +195,8 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
         it.q_end = it.q_live = p.q_rows;
         if (p.offsets) {
             o = seg_start(p, lo, p.q_rows);
-            it.q_end = lo + 1 == p.groups ? min(__ldg(p.offsets + lo + 1), p.q_rows) : seg_start(p, lo + 1, p.q_rows);
-            it.q_live = o + min(max(0, it.q_end - o), max(0, __ldg(p.counts + lo)));
+            it.q_end = lo + 1 == p.groups ? min(*(p.offsets + lo + 1), p.q_rows) : seg_start(p, lo + 1, p.q_rows);
+            it.q_live = o + min(max(0, it.q_end - o), max(0, *(p.counts + lo)));
         }
         it.q0 = o + q_tile * TQ;
         it.b0 = 0;
@@ -231,7 +232,7 @@ __device__ __forceinline__ LinShare lin_share(const LinParams& p, const LinItem&
     e.end = max(0, it.q_end - q);
     e.live = max(0, min(it.q_live - q, e.end));
     e.f = f;
-    e.bias = p.bias && f < p.p_rows ? __ldg(p.bias + (size_t)it.group * p.p_rows + f) : 0.f;
+    e.bias = p.bias && f < p.p_rows ? p.bias[(size_t)it.group * p.p_rows + f] : 0.f;
     return e;
 }
 
@@ -293,11 +294,11 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
         uint32_t w[NC / 2];
         if (j0 + NC <= e.live) {
 #pragma unroll
-            for (int j = 0; j < NC; j += 2, r += step) w[j / 2] = __ldg(reinterpret_cast<const uint32_t*>(r));
+            for (int j = 0; j < NC; j += 2, r += step) w[j / 2] = ld_nc_u32(r);
         } else {
 #pragma unroll
             for (int j = 0; j < NC; j += 2, r += step)
-                w[j / 2] = j < left ? __ldg(reinterpret_cast<const uint32_t*>(r)) : 0u;
+                w[j / 2] = j < left ? ld_nc_u32(r) : 0u;
         }
 #pragma unroll
         for (int j = 0; j < NC; j += 2) {
@@ -399,6 +400,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             tmem_relinquish();
         }
     }
+    // (everything above touches this CTA's own memory only)
+    grid_wait();
     if (warp == 3) {
         // first tile of every group
         if (p.by_contraction) {
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     int len = p.q_rows;
                     if (p.offsets) {
                         const int lo = seg_start(p, g, p.q_rows);
-                        const int hi = min(__ldg(p.offsets + g + 1), p.q_rows);
+                        const int hi = min(*(p.offsets + g + 1), p.q_rows);
                         len = max(0, hi - lo);
                     }
                     n = (len + TQ - 1) / TQ * p.pt;
@@ -433,6 +436,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         }
     }
     __syncthreads();
+    grid_launch_next();   // (tensor memory is allocated: the next kernel's CTAs cannot take it first)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem;
     const int total = ctl->total;
@@ -756,27 +760,10 @@ template <int TQ>
 cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q32, int ctas,
                       cudaStream_t stream) {
     using C = LinCfg<TQ>;
-    // (once per device: the call costs more than the launch)
-    static unsigned long long ready = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!(__atomic_load_n(&ready, __ATOMIC_ACQUIRE) >> dev & 1)) {
-        e = cudaFuncSetAttribute(linear_kernel<TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::ctl_bytes());
-        if (e != cudaSuccess) return e;
-        __atomic_fetch_or(&ready, 1ull << dev, __ATOMIC_RELEASE);
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::ctl_bytes();
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)(C::kPair ? 2 : p.splits), 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = C::kPair || p.splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<TQ>, p, map_p, map_q, map_q32);
+    static unsigned long long allowed = 0;
+    if (cudaError_t e = allow_smem(linear_kernel<TQ>, C::ctl_bytes(), allowed)) return e;
+    return launch(linear_kernel<TQ>, dim3((unsigned)ctas), C::kThreads, C::ctl_bytes(), C::kPair ? 2 : p.splits, stream, p, map_p,
+                  map_q, map_q32);
 }
 
 }  // namespace

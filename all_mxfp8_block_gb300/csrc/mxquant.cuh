@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "kernels.cuh"
+#include "ptx.cuh"
 
 namespace mxa2a {
 
@@ -37,16 +38,31 @@ template <typename T, int V>
 struct Vec {
     static_assert(V == 1 || (V * sizeof(T)) % 16 == 0, "vector width");
     static constexpr int kWords = V * (int)sizeof(T) / 16;
-    __device__ static __forceinline__ void load(const T* p, float (&f)[V]) {
+    // as loaded: half the registers of the fp32 values for 16-bit types
+    struct Raw {
+        uint4 w[V == 1 ? 1 : kWords];
+    };
+    __device__ static __forceinline__ Raw raw(const T* p) {
+        Raw r;
         if constexpr (V == 1) {
-            f[0] = (float)*p;
+            r.w[0].x = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
         } else {
-            uint4 w[kWords];
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-            unpack(w, f);
+            for (int i = 0; i < kWords; ++i) r.w[i] = ptx::ld_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+        }
+        return r;
+    }
+    __device__ static __forceinline__ void values(const Raw& r, float (&f)[V]) {
+        if constexpr (V > 1) {
+            unpack(r.w, f);
+        } else if constexpr (sizeof(T) == 4) {
+            f[0] = __uint_as_float(r.w[0].x);
+        } else {
+            const uint16_t h = (uint16_t)r.w[0].x;
+            f[0] = (float)*reinterpret_cast<const T*>(&h);
         }
     }
+    __device__ static __forceinline__ void load(const T* p, float (&f)[V]) { values(raw(p), f); }
     __device__ static __forceinline__ void unpack(const uint4* w, float (&f)[V]) {
         const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
         if constexpr (sizeof(T) == 4) {

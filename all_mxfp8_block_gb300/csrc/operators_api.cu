@@ -61,7 +61,9 @@ constexpr int64_t kMaxHidden = int64_t(1) << 20;
 // the size rules shared by the row operators
 bool moe_shape(int64_t tokens, int topk, int experts, int64_t hidden, int64_t rows) {
     return tokens >= 0 && topk >= 1 && topk <= 64 && experts >= 1 && experts <= 1024 && tokens <= kMaxAssignments / topk &&
-           hidden >= 1 && hidden <= kMaxHidden && rows >= 0 && rows <= kMaxRows;
+           hidden >= 1 && hidden <= kMaxHidden && rows >= 0 && rows <= kMaxRows &&
+           // (a launch's blocks, at most one per 256 elements of a row, are counted in 32 bits)
+           tokens * ((hidden + 255) / 256) <= kMaxRows - 8192;
 }
 
 }  // namespace

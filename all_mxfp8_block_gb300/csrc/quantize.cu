@@ -3,6 +3,7 @@
 // in the same pass, and the reordering of plain scale rows into scale tiles.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "moe.cuh"
 #include "mxquant.cuh"
 
@@ -26,10 +27,10 @@ __device__ __forceinline__ bool row_is_token(const Segments& s, long long r) {
     int lo = 0, hi = s.experts - 1;   // the last e with offsets[e] <= r
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(s.offsets + mid) <= r) lo = mid; else hi = mid - 1;
+        if (s.offsets[mid] <= r) lo = mid; else hi = mid - 1;
     }
-    const long long o = __ldg(s.offsets + lo);
-    return r >= o && r < o + __ldg(s.counts + lo);
+    const long long o = s.offsets[lo];
+    return r >= o && r < o + s.counts[lo];
 }
 
 __device__ __forceinline__ float abs_max(float m, float v) { return max_nan(m, fabsf(v)); }
@@ -45,8 +46,10 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     const bool e5m2 = q.e5m2;
     const int emax = mx_emax(e5m2);
     const bool masked = q.seg.offsets != nullptr;
+    grid_wait();
+    grid_launch_next();
     if (masked) {
-        if (r0 >= __ldg(q.seg.offsets + q.seg.experts)) return;   // past the last segment: nothing is read from there
+        if (r0 >= q.seg.offsets[q.seg.experts]) return;   // past the last segment: nothing is read from there
         if (threadIdx.x < kTileRows)
             token[threadIdx.x] = r0 + threadIdx.x < q.rows && row_is_token(q.seg, r0 + threadIdx.x);
         __syncthreads();
@@ -73,8 +76,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
         uint4 zw[kPass];
 #pragma unroll
         for (int p = 0; p < kPass; ++p)
-            zw[p] = live[p] ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(q.preact) +
-                                                                   (r0 + ty + p * 32) * q.cols + col))
+            zw[p] = live[p] ? ptx::ld_nc_v4(static_cast<const __nv_bfloat16*>(q.preact) + (r0 + ty + p * 32) * q.cols + col)
                             : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
@@ -175,14 +177,16 @@ __global__ void __launch_bounds__(256) bias_sums_kernel(const float* colsum, Seg
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = blockIdx.y;
     const long long c = (long long)blockIdx.x * 32 + lane;   // (columns come in blocks of 32)
     long long lo = 0, hi = (s.rows + 31) / 32;
+    grid_wait();
+    grid_launch_next();
     if (s.offsets) {
-        lo = max(0, __ldg(s.offsets + g)) / 32;
-        hi = min(hi, (long long)__ldg(s.offsets + g + 1) / 32);
+        lo = max(0, s.offsets[g]) / 32;
+        hi = min(hi, (long long)s.offsets[g + 1] / 32);
     }
     const long long per = (max(0ll, hi - lo) + 7) / 8, b1 = min(hi, lo + (warp + 1) * per);
     float sum = 0.f;
 #pragma unroll 8
-    for (long long b = lo + warp * per; b < b1; ++b) sum += __ldg(colsum + b * cols + c);
+    for (long long b = lo + warp * per; b < b1; ++b) sum += colsum[b * cols + c];
     part[warp][lane] = sum;
     __syncthreads();
     if (warp == 0) {
@@ -194,6 +198,8 @@ __global__ void __launch_bounds__(256) bias_sums_kernel(const float* colsum, Seg
 
 __global__ void scale_tiles_kernel(const uint8_t* s, int groups, long long rows, long long blocks, uint32_t* tiles, int rt, int bt) {
     const long long per = (long long)bt * rt * 128, n = per * groups;
+    grid_wait();
+    grid_launch_next();
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
         const long long g = i / per, j = i % per;
         const int w = (int)(j % 128), row_tile = (int)(j / 128 % rt), kb = (int)(j / 128 / rt);
@@ -211,32 +217,28 @@ cudaError_t launch_quantize(const Quantize& q, cudaStream_t stream) {
     const int row_tiles = (int)((q.rows + kTileRows - 1) / kTileRows);
     const dim3 grid((unsigned)((long long)row_tiles * q.groups), (unsigned)((q.cols + kTileCols - 1) / kTileCols));
     if (q.x_type == kTypeF16)
-        quantize_kernel<__half, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else if (q.x_type == kTypeF32)
-        quantize_kernel<float, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else if (!q.preact)
-        quantize_kernel<__nv_bfloat16, kActNone><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else if (q.act == kActRelu)
-        quantize_kernel<__nv_bfloat16, kActRelu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else if (q.act == kActGelu)
-        quantize_kernel<__nv_bfloat16, kActGelu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    else
-        quantize_kernel<__nv_bfloat16, kActSilu><<<grid, kQThreads, 0, stream>>>(q, row_tiles);
-    return cudaGetLastError();
+        return launch(quantize_kernel<__half, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    if (q.x_type == kTypeF32)
+        return launch(quantize_kernel<float, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    if (!q.preact)
+        return launch(quantize_kernel<__nv_bfloat16, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    if (q.act == kActRelu)
+        return launch(quantize_kernel<__nv_bfloat16, kActRelu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    if (q.act == kActGelu)
+        return launch(quantize_kernel<__nv_bfloat16, kActGelu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    return launch(quantize_kernel<__nv_bfloat16, kActSilu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
 }
 
 cudaError_t launch_bias_sums(const float* colsum, const Segments& seg, long long cols, float* dbias, cudaStream_t stream) {
     const dim3 grid((unsigned)(cols / 32), (unsigned)seg.experts);
-    bias_sums_kernel<<<grid, 256, 0, stream>>>(colsum, seg, cols, dbias);
-    return cudaGetLastError();
+    return launch(bias_sums_kernel, grid, 256, 0, 1, stream, colsum, seg, cols, dbias);
 }
 
 cudaError_t launch_scale_tiles(const uint8_t* s, int groups, long long rows, long long blocks, uint8_t* tiles, cudaStream_t stream) {
     const int rt = (int)((rows + 127) / 128), bt = (int)((blocks + 3) / 4);
     const long long words = (long long)groups * rt * bt * 128;
-    scale_tiles_kernel<<<(unsigned)std::min<long long>((words + 255) / 256, 152 * 16), 256, 0, stream>>>(
-        s, groups, rows, blocks, reinterpret_cast<uint32_t*>(tiles), rt, bt);
-    return cudaGetLastError();
+    return launch(scale_tiles_kernel, dim3((unsigned)std::min<long long>((words + 255) / 256, 152 * 16)), 256, 0, 1, stream, s, groups,
+                  rows, blocks, reinterpret_cast<uint32_t*>(tiles), rt, bt);
 }
 
 }  // namespace mxa2a
