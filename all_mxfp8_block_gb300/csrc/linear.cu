@@ -16,9 +16,9 @@
 // persistent over tiles.  The widest tile is computed by CTA pairs: 256 P rows x
 // 256 Q rows, the even CTA issuing the MMAs of both; a tile's MMAs are only as
 // wide as its segment needs.  With few tiles a cluster of up to 8 CTAs shares a
-// tile's contraction: each accumulates its part, the partial tiles meet in
-// distributed shared memory and every CTA sums (in rank order) and finishes
-// its share of the columns, in the same launch.
+// tile's contraction: each accumulates its part and writes every column's
+// partial sums to the shared memory of the CTA that finishes the column, which
+// adds them in rank order, in the same launch.
 //
 // Segments start at multiples of 32 rows, so a token tile may start inside a
 // 128-row scale tile: the scale warps shift the columns while they copy.  A
@@ -42,6 +42,16 @@ namespace {
 constexpr int kMaxGroups = 1024;
 constexpr int kLinMaxStages = 6;
 
+// 32 lanes x 4 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
 // 32 lanes x 16 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -57,7 +67,10 @@ struct LinCfg {
     // MMA stream (cta_group::2), each holding its 128 P rows and half of the Q
     // rows, so a stage moves and reads a third less shared memory per MMA.
     static constexpr bool kPair = TQ == 256;
-    static constexpr int kStages = kPair ? 5 : (TQ == 128 ? 6 : 4);
+    // stages of the ring, and those of a launch whose CTAs share tiles: the others' part of the tile lands
+    // behind them (all but this CTA's own share of at most 8: 7/8 of [TQ][128] fp32)
+    static constexpr int kStages = kPair ? 5 : (TQ == 128 ? 6 : TQ == 64 ? 4 : 5);
+    static constexpr int kSplitStages = TQ == 64 ? 3 : 4;
     static constexpr int kCtasPerSm = TQ <= 64 ? 2 : 1;
     static constexpr int kEpiWarps = TQ >= 128 ? 8 : 4;
     static constexpr int kThreads = 256 + 32 * kEpiWarps;
@@ -75,15 +88,14 @@ struct LinCfg {
     static constexpr int kQRows = kPair ? 128 : TQ;                                 // Q rows this CTA holds of a tile
     static constexpr int kQBytes = kQRows * 128;
     static constexpr int kColsPerWarp = TQ / (kEpiWarps / 4);
-    static constexpr size_t oP = 0;
-    static constexpr size_t oQ = oP + (size_t)kStages * kAStageBytes;
-    static constexpr size_t oSfp = oQ + (size_t)kStages * kQBytes;
+    static constexpr int kStageBytes = kAStageBytes + kQBytes;
+    static constexpr size_t oPart = (size_t)kSplitStages * kStageBytes;
+    static constexpr size_t kPartBytes = kPair ? 0 : (size_t)TQ * 512 / 8 * 7;
+    static constexpr size_t oSfp = (size_t)kStages * kStageBytes > oPart + kPartBytes ? (size_t)kStages * kStageBytes : oPart + kPartBytes;
     static constexpr size_t oSfq = oSfp + (size_t)kStages * 512;
     static constexpr size_t oCtl = oSfq + (size_t)kStages * kQAtoms * 512;
     static constexpr size_t ctl_bytes();
     static_assert(kSfCol + kStages * kSfCols <= kTmem, "tensor memory columns");
-    // a split tile's fp32 partial [TQ][128] lies over the stages, which its MMAs have read
-    static_assert(kPair || TQ * 512 <= kStages * (kAStageBytes + kQBytes), "partial tile");
 };
 
 struct __align__(8) LinCtl {
@@ -161,15 +173,16 @@ __device__ __forceinline__ int seg_start(const LinParams& p, int g, int limit) {
 template <int TQ>
 __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ctl, int tile, int rank) {
     LinItem it;
-    int p_tile, q_tile;
+    int p_tile, q_tile, qt;
     if (p.by_contraction) {
         const int per = p.pt * p.qt;
         it.group = tile / per;
         const int r = tile - it.group * per;
         q_tile = r / p.pt;
         p_tile = r - q_tile * p.pt;
-        it.q0 = q_tile * TQ;
+        it.q0 = 0;
         it.q_end = it.q_live = p.q_rows;
+        qt = p.qt;
         it.b0 = 0;
         it.b1 = p.blocks;
         if (p.offsets) {
@@ -183,7 +196,8 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
             if (ctl->start[mid] <= tile) lo = mid; else hi = mid - 1;
         }
         it.group = lo;
-        const int first = ctl->start[lo], qt = (ctl->start[lo + 1] - first) / p.pt;
+        const int first = ctl->start[lo];
+        qt = (ctl->start[lo + 1] - first) / p.pt;
         const int r = tile - first;
         // bands of 2048 P rows, all Q tiles of a band before the next: the CTAs
         // in flight share P and Q tiles in L2
@@ -198,10 +212,16 @@ __device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ct
             it.q_end = lo + 1 == p.groups ? min(*(p.offsets + lo + 1), p.q_rows) : seg_start(p, lo + 1, p.q_rows);
             it.q_live = o + min(max(0, it.q_end - o), max(0, *(p.counts + lo)));
         }
-        it.q0 = o + q_tile * TQ;
+        it.q0 = o;
         it.b0 = 0;
         it.b1 = p.blocks;
     }
+    // the segment's tiles are equally wide, in 32-row steps (none is empty: the
+    // width is at most TQ): no narrow last tile that costs a stage's latency for
+    // little work
+    const int width = ((it.q_end - it.q0 + qt - 1) / qt + 31) & ~31;
+    it.q0 += q_tile * width;
+    it.q_end = min(it.q_end, it.q0 + width);
     it.p0 = p_tile * (LinCfg<TQ>::kPair ? 256 : 128) + (LinCfg<TQ>::kPair ? rank * 128 : 0);
     it.nq = max(32, min(TQ, (it.q_end - it.q0 + 31) & ~31));   // (a tile past its segment's end, which only foreign offsets make: nothing is stored)
     const int lo = it.b0 / 4, hi = it.b1 > it.b0 ? (it.b1 + 3) / 4 : lo;
@@ -358,6 +378,13 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The cluster barriers of a shared tile: the parts have been written to their
+// owners; before the next tile's, they have been read.
+__device__ __forceinline__ void lin_tile_end(bool more) {
+    cluster_sync();
+    if (more) cluster_sync();
+}
+
 template <int TQ>
 __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     linear_kernel(const __grid_constant__ LinParams p, const __grid_constant__ CUtensorMap map_p,
@@ -369,6 +396,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     LinCtl* ctl = reinterpret_cast<LinCtl*>(smem + C::oCtl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const bool split = !kPair && p.splits > 1;
+    const int stages = split ? C::kSplitStages : C::kStages;
     const int share = kPair ? 2 : p.splits;      // CTAs to a tile
     const int rank = kPair || split ? (int)cluster_ctarank() : 0;
     const int first = (int)blockIdx.x / share, stride = (int)gridDim.x / share;
@@ -446,7 +474,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
     if (warp == 0 || warp == 2) {
         // ---------------------------------------------------------- TMA producers
         const int pid = warp / 2;
-        int n = 0;
+        int n = 0, stage = 0;
+        uint32_t ph = 0;
         // (pair: both CTAs' loads of a stage complete on the even CTA's barrier,
         // which its producer arms for the bytes of both)
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
@@ -460,43 +489,44 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             const int half = it.nq / 2, boxes = (half + 31) / 32;               // pair: Q rows of each CTA, in boxes of 32
             if (lane == 0) {
                 for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                    if ((n & 1) != pid) continue;
-                    const int stage = n % C::kStages;
-                    if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ((n / C::kStages) & 1) ^ 1, kRoleTma)) break;
-                    mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
-                    bulk_load(smem + C::oSfp + stage * 512,
-                              p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
-                                  ((size_t)kb * p.p_row_tiles + pa) * 512,
-                              512, &ctl->sf_full[stage]);
-                    bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512,
-                              p.q_scale + ((size_t)kb * p.q_row_tiles + qa) * 512, 512 * atoms, &ctl->sf_full[stage]);
-                    uint8_t* pd = smem + C::oP + (size_t)stage * kAStageBytes;
-                    uint8_t* qd = smem + C::oQ + (size_t)stage * C::kQBytes;
-                    if constexpr (kPair) {
-                        const bool whole = it.nq == TQ;
-                        const uint32_t bytes = kAStageBytes + (whole ? C::kQBytes : boxes * 32 * 128);
-                        const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
-                        if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
-                        tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
-                        const int qy = it.q0 + rank * half;
-                        if (whole)
-                            tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
-                        else
-                            for (int b = 0; b < boxes; ++b)
-                                tma_load_2d_pair(qd + b * 4096, &map_q32, bar, kb * 128, qy + b * 32, keep);
-                    } else {
-                        mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
-                        tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
-                        tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, it.q0);
+                    if ((n & 1) == pid) {
+                        if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ph ^ 1, kRoleTma)) break;
+                        uint8_t* pd = smem + (size_t)stage * C::kStageBytes;
+                        uint8_t* qd = pd + kAStageBytes;
+                        mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
+                        bulk_load(smem + C::oSfp + stage * 512,
+                                  p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
+                                      ((size_t)kb * p.p_row_tiles + pa) * 512,
+                                  512, &ctl->sf_full[stage]);
+                        bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512,
+                                  p.q_scale + ((size_t)kb * p.q_row_tiles + qa) * 512, 512 * atoms, &ctl->sf_full[stage]);
+                        if constexpr (kPair) {
+                            const bool whole = it.nq == TQ;
+                            const uint32_t bytes = kAStageBytes + (whole ? C::kQBytes : boxes * 32 * 128);
+                            const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
+                            if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
+                            tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
+                            const int qy = it.q0 + rank * half;
+                            if (whole)
+                                tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
+                            else
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d_pair(qd + b * 4096, &map_q32, bar, kb * 128, qy + b * 32, keep);
+                        } else {
+                            mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
+                            tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
+                            tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, it.q0);
+                        }
+                        ctl->issued[pid] = n + 1;
                     }
-                    ctl->issued[pid] = n + 1;
+                    if (++stage == stages) {
+                        stage = 0;
+                        ph ^= 1;
+                    }
                 }
             }
             __syncwarp();
-            if (split) {
-                cluster_sync();
-                cluster_sync();
-            }
+            if (split) lin_tile_end(tile + stride < total);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer (pair: the even CTA's, for both)
@@ -504,8 +534,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // instruction here counts once per stage): one wait, no other shared-memory
         // access, the descriptors by addition.
         const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | (1u << 23) | ((kPair ? 16u : 8u) << 24);
-        const uint64_t ad0 = smem_desc(smem_u32(smem + C::oP), 16, 1024, kLayoutSw128);
-        const uint64_t bd0 = smem_desc(smem_u32(smem + C::oQ), 16, 1024, kLayoutSw128);
+        const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSw128);
+        const uint64_t bd0 = smem_desc(smem_u32(smem + kAStageBytes), 16, 1024, kLayoutSw128);
         int stage = 0, acc = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
@@ -523,8 +553,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     if (!lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
-                    const uint64_t ad = ad0 + (uint32_t)(stage * (kAStageBytes >> 4));
-                    const uint64_t bd = bd0 + (uint32_t)(stage * (C::kQBytes >> 4));
+                    const uint64_t ad = ad0 + (uint32_t)(stage * (C::kStageBytes >> 4));
+                    const uint64_t bd = bd0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     auto step = [&](int k) {   // 32 of the contraction: +32 bytes inside the swizzled 128, scale byte k
                         const uint32_t idesc = idesc1 | ((uint32_t)k << 4) | ((uint32_t)k << 29);
                         if constexpr (kPair)
@@ -543,7 +573,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                         tc_commit_pair_multicast(&ctl->empty[stage], 0x3);
                     else
                         tc_commit(&ctl->empty[stage]);
-                    if (++stage == C::kStages) {
+                    if (++stage == stages) {
                         stage = 0;
                         ph ^= 1;
                     }
@@ -555,22 +585,19 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 ++acc;
             }
             __syncwarp();
-            if (split) {
-                cluster_sync();
-                cluster_sync();
-            }
+            if (split) lin_tile_end(tile + stride < total);
         }
     } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------- scale warps
         const int quarter = warp & 3;
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
-        int n = 0;
+        int stage = 0;
+        uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
-            for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                const int stage = n % C::kStages;
-                lin_wait(p, ctl, &ctl->sf_full[stage], (n / C::kStages) & 1, kRoleScale);
+            for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                lin_wait(p, ctl, &ctl->sf_full[stage], ph, kRoleScale);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)stage * C::kSfCols;
@@ -601,17 +628,20 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     else
                         mbar_arrive_remote_relaxed(full0 + (uint32_t)stage * sizeof(uint64_t));
                 }
+                if (++stage == stages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
             }
             __syncwarp();
-            if (split) {
-                cluster_sync();
-                cluster_sync();
-            }
+            if (split) lin_tile_end(tile + stride < total);
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------- epilogue
         const int quarter = warp & 3, part = (warp - 8) >> 2;
-        float* partial = reinterpret_cast<float*>(smem);   // [TQ][128]: the split tiles' (over the stages)
+        // shared tiles: the others' parts of this CTA's columns, [splits - 1][TQ / splits][128] fp32
+        const float* parts_in = reinterpret_cast<const float*>(smem + C::oPart);
+        const int own = split ? TQ / p.splits : TQ;
         int acc = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
@@ -677,25 +707,60 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     ++acc;
                 }
             } else {
+                if (!split) {
 #pragma unroll 1
-                for (int c = 0; c < C::kColsPerWarp; c += 16) {
-                    float v[16];
-                    if (live) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(t + (uint32_t)c, r);
-                        tc_wait_ld();
+                    for (int c = 0; c < C::kColsPerWarp; c += 16) {
+                        float v[16];
+                        if (live) {
+                            tmem_ld_32x32b_x16(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[16]>(v));
+                            tc_wait_ld();
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        }
+                        if (in_p) lin_store<16>(p, e, c, lane, v);
                     }
-                    if (split) {
+                } else {
+                    // every 4 columns to the CTA that finishes them
+#pragma unroll 1
+                    for (int c = part * C::kColsPerWarp; c < (part + 1) * C::kColsPerWarp; c += 4) {
+                        const int to = c / own;
+                        if (to == rank) continue;
+                        float v[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (live) {
+                            tmem_ld_32x32b_x4(t + (uint32_t)(c - part * C::kColsPerWarp), *reinterpret_cast<uint32_t(*)[4]>(v));
+                            tc_wait_ld();
+                        }
+                        const int slot = rank < to ? rank : rank - 1;
+                        const uint32_t at = mapa_shared(smem_u32(parts_in + (slot * own + c - to * own) * 128 + quarter * 32 + lane), to);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) partial[(part * C::kColsPerWarp + c + j) * 128 + quarter * 32 + lane] = v[j];
-                    } else if (in_p) {
-                        lin_store<16>(p, e, c, lane, v);
+                        for (int j = 0; j < 4; ++j) st_shared_cluster_f32(at + j * 512, v[j]);
                     }
+                    __syncwarp();
+                    cluster_sync();
+                    // this CTA's columns, the parts added in rank order
+                    const LinShare whole = lin_share(p, it, f, 0);
+                    for (int c = rank * own + part * 4; c < (rank + 1) * own; c += 4 * (C::kEpiWarps / 4)) {
+                        float mine[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (live) {
+                            tmem_ld_32x32b_x4(t + (uint32_t)(c - part * C::kColsPerWarp), *reinterpret_cast<uint32_t(*)[4]>(mine));
+                            tc_wait_ld();
+                        }
+                        const float* in = parts_in + (c - rank * own) * 128 + quarter * 32 + lane;
+                        for (int s = 0; s < p.splits; ++s) {
+                            if (s == rank) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) v[j] += mine[j];
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) v[j] += in[j * 128];
+                                in += own * 128;
+                            }
+                        }
+                        if (in_p) lin_store<4>(p, whole, c, lane, v);
+                    }
+                    __syncwarp();
+                    if (tile + stride < total) cluster_sync();
                 }
                 if (live) {
                     tc_fence_before();
@@ -703,32 +768,10 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     if (lane == 0) mbar_arrive(&ctl->acc_empty[buf]);
                     ++acc;
                 }
-                if (split) {
-                    __syncwarp();
-                    cluster_sync();
-                    // this CTA's share of the columns, 4 at a time over the epilogue's column parts
-                    const int cols = TQ / p.splits, parts = C::kEpiWarps / 4;
-                    const LinShare whole = lin_share(p, it, f, 0);
-                    for (int c = rank * cols + part * 4; in_p && c < (rank + 1) * cols; c += 4 * parts) {
-                        float v[4] = {0.f, 0.f, 0.f, 0.f};
-                        for (int s = 0; s < p.splits; ++s) {
-                            const uint32_t at = mapa_shared(smem_u32(partial + c * 128 + quarter * 32 + lane), s);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) v[j] += __uint_as_float(ld_shared_cluster_u32(at + j * 512));
-                        }
-                        lin_store<4>(p, whole, c, lane, v);
-                    }
-                    fence_proxy_async_shared();   // (this thread's writes, before TMA fills the stages again)
-                    __syncwarp();
-                    cluster_sync();   // the partial tiles have been read: the stages may be filled again
-                }
             }
         }
     } else if (split) {
-        for (int tile = first; tile < total; tile += stride) {
-            cluster_sync();
-            cluster_sync();
-        }
+        for (int tile = first; tile < total; tile += stride) lin_tile_end(tile + stride < total);
     }
     __syncthreads();
     if (ctl->abort && threadIdx.x == 0) {
@@ -736,12 +779,12 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // time to land (bounded) before the CTA ends (pair: the even CTA's
         // barrier counts both CTAs' loads, and both end together below)
         const uint64_t t0 = globaltimer();
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             const int last = max(ctl->issued[0], ctl->issued[1]) - 1;
-            const int n = last - ((last - s) % C::kStages + C::kStages) % C::kStages;   // stage s's last use
+            const int n = last - ((last - s) % stages + stages) % stages;   // stage s's last use
             if (n < 0) continue;
-            while (!((kPair && rank != 0) || lin_try<kPair>(&ctl->full[s], (n / C::kStages) & 1)) ||
-                   !mbar_try_wait(&ctl->sf_full[s], (n / C::kStages) & 1))
+            while (!((kPair && rank != 0) || lin_try<kPair>(&ctl->full[s], (n / stages) & 1)) ||
+                   !mbar_try_wait(&ctl->sf_full[s], (n / stages) & 1))
                 if (globaltimer() - t0 > (uint64_t)p.timeout_ns) break;
         }
     }
