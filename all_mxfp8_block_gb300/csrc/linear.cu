@@ -371,6 +371,11 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
     }
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // arrive on a barrier of another CTA without ordering earlier memory accesses (a
 // release waits for every earlier global store, about 1 us; what the barrier
 // hands over is tensor memory, whose accesses are complete: tcgen05.wait::st / ::ld)
@@ -536,52 +541,62 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | (1u << 23) | ((kPair ? 16u : 8u) << 24);
         const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSw128);
         const uint64_t bd0 = smem_desc(smem_u32(smem + kAStageBytes), 16, 1024, kLayoutSw128);
+        // The whole warp walks the loop (the descriptors stay in uniform registers),
+        // one elected lane issues.
+        const bool leader = elect_one();
         int stage = 0, acc = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
-            if (lane == 0 && it.kb1 > it.kb0) {
+            if (it.kb1 > it.kb0) {
                 const int buf = acc & 1;
                 lin_wait<kPair>(p, ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
                 if (C::kOverlap && acc) lin_wait<kPair>(p, ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * C::kAccStep);
                 const uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
-                uint32_t some = 0;
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (C::kStageBytes >> 4));
-                    auto step = [&](int k) {   // 32 of the contraction: +32 bytes inside the swizzled 128, scale byte k
-                        const uint32_t idesc = idesc1 | ((uint32_t)k << 4) | ((uint32_t)k << 29);
+                    const int k0 = max(0, it.b0 - kb * 4), k1 = min(4, it.b1 - kb * 4);
+                    if (leader) {
+                        auto step = [&](int k, uint32_t add) {   // 32 of the contraction: +32 bytes inside the swizzled 128, scale byte k
+                            const uint32_t idesc = idesc1 | ((uint32_t)k << 4) | ((uint32_t)k << 29);
+                            if constexpr (kPair)
+                                mma_mxf8f6f4_pair(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, add);
+                            else
+                                mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, add);
+                        };
+                        const uint32_t later = kb != it.kb0;
+                        if (k1 - k0 == 4) {
+                            step(0, later);
+                            step(1, 1);
+                            step(2, 1);
+                            step(3, 1);
+                        } else {   // a range that starts or ends inside the block
+                            for (int k = k0; k < k1; ++k) step(k, later | (uint32_t)(k > k0));
+                        }
                         if constexpr (kPair)
-                            mma_mxf8f6f4_pair(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
+                            tc_commit_pair_multicast(&ctl->empty[stage], 0x3);
                         else
-                            mma_mxf8f6f4(d, ad + 2ull * k, bd + 2ull * k, idesc, sf, sf + 4, some);
-                        some = 1;
-                    };
-                    if (kb * 4 >= it.b0 && kb * 4 + 4 <= it.b1) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) step(k);
-                    } else {   // a range that starts or ends inside the block
-                        for (int k = max(0, it.b0 - kb * 4); k < min(4, it.b1 - kb * 4); ++k) step(k);
+                            tc_commit(&ctl->empty[stage]);
                     }
-                    if constexpr (kPair)
-                        tc_commit_pair_multicast(&ctl->empty[stage], 0x3);
-                    else
-                        tc_commit(&ctl->empty[stage]);
+                    __syncwarp();
                     if (++stage == stages) {
                         stage = 0;
                         ph ^= 1;
                     }
                 }
-                if constexpr (kPair)
-                    tc_commit_pair_multicast(&ctl->acc_full[buf], 0x3);
-                else
-                    tc_commit(&ctl->acc_full[buf]);
+                if (leader) {
+                    if constexpr (kPair)
+                        tc_commit_pair_multicast(&ctl->acc_full[buf], 0x3);
+                    else
+                        tc_commit(&ctl->acc_full[buf]);
+                }
                 ++acc;
             }
             __syncwarp();
