@@ -8,7 +8,7 @@
 // decode step's few tokens then cost a 32-column tile, the weights stream
 // through once, and an output row is written by neighbouring lanes.
 //
-// CTA roles: warps 0 and 2 issue the TMA loads (even / odd stages), warp 1 owns
+// CTA roles: warps 0, 2 and 3 issue the TMA loads (the stages in turn), warp 1 owns
 // the tensor memory and issues the MMAs, warps 4-7 move the stages' scale bytes
 // into tensor memory (one warp per lane quarter), the warps from 8 on are the
 // epilogue.  A stage is one 128-wide block of the contraction: 128 P rows,
@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kMaxGroups = 1024;
 constexpr int kLinMaxStages = 6;
+constexpr int kProd = 3;   // producer warps: 0, 2 and 3
 
 // 32 lanes x 4 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[4]) {
@@ -69,7 +70,7 @@ struct LinCfg {
     static constexpr bool kPair = TQ == 256;
     // stages of the ring, and those of a launch whose CTAs share tiles: the others' part of the tile lands
     // behind them (all but this CTA's own share of at most 8: 7/8 of [TQ][128] fp32)
-    static constexpr int kStages = kPair ? 5 : (TQ == 128 ? 6 : TQ == 64 ? 4 : 5);
+    static constexpr int kStages = kPair ? 5 : TQ == 128 ? 6 : TQ == 64 ? 4 : 5;
     static constexpr int kSplitStages = TQ == 64 ? 3 : 4;
     static constexpr int kCtasPerSm = TQ <= 64 ? 2 : 1;
     static constexpr int kEpiWarps = TQ >= 128 ? 8 : 4;
@@ -84,6 +85,8 @@ struct LinCfg {
     static constexpr int kQCols = TQ / 32 < 4 ? 4 : TQ / 32;                        // TMEM columns of its scales
     static constexpr uint32_t kSfCol = kAccStep + TQ;
     static constexpr uint32_t kSfCols = 4 + kQCols;
+    // stages whose scales are in tensor memory (the pair kernel has columns left for 5 of its 6)
+    static constexpr int kSfSlots = kPair ? 5 : kStages;
     static constexpr uint32_t kTmem = TQ <= 32 ? 128 : (TQ == 64 ? 256 : 512);
     static constexpr int kQRows = kPair ? 128 : TQ;                                 // Q rows this CTA holds of a tile
     static constexpr int kQBytes = kQRows * 128;
@@ -95,7 +98,7 @@ struct LinCfg {
     static constexpr size_t oSfq = oSfp + (size_t)kStages * 512;
     static constexpr size_t oCtl = oSfq + (size_t)kStages * kQAtoms * 512;
     static constexpr size_t ctl_bytes();
-    static_assert(kSfCol + kStages * kSfCols <= kTmem, "tensor memory columns");
+    static_assert(kSfCol + kSfSlots * kSfCols <= kTmem, "tensor memory columns");
 };
 
 struct __align__(8) LinCtl {
@@ -106,7 +109,7 @@ struct __align__(8) LinCtl {
     uint64_t acc_part[2];                 // its columns that the other accumulator shares are read
     uint32_t tmem;
     volatile int abort;
-    volatile int issued[2];           // stages issued by each producer
+    volatile int issued[3];           // stages issued by each producer
     int total;                        // tiles of all groups
     int start[kMaxGroups + 1];        // first tile of each group (grouped Q rows)
 };
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             mbar_init(&ctl->acc_part[b], C::kEpiWarps);   // (half of either CTA's epilogue warps)
         }
         ctl->abort = 0;
-        ctl->issued[0] = ctl->issued[1] = 0;
+        ctl->issued[0] = ctl->issued[1] = ctl->issued[2] = 0;
         fence_mbarrier_init();
         prefetch_tensormap(&map_p);
         prefetch_tensormap(&map_q);
@@ -476,13 +479,15 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 
     if (kPair || split) cluster_sync();   // every CTA of the cluster runs before any touches its shared memory
 
-    if (warp == 0 || warp == 2) {
-        // ---------------------------------------------------------- TMA producers
-        const int pid = warp / 2;
+    if (warp == 0 || (warp >= 2 && warp <= kProd)) {
+        // ---------------------------------------------------------- TMA producers: the stages in turn
+        const bool leader = elect_one();
+        const int pid = warp ? warp - 1 : 0;
+        int turn = pid;
         int n = 0, stage = 0;
         uint32_t ph = 0;
         // (pair: both CTAs' loads of a stage complete on the even CTA's barrier,
-        // which its producer arms for the bytes of both)
+        // which its P producer arms for the bytes of both)
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
         const uint64_t keep = l2_policy_evict_last();
         for (int tile = first; tile < total; tile += stride) {
@@ -492,42 +497,44 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             const int pa = min(it.p0 >> 7, p.p_row_tiles - 1);                  // (a pair's second half may lie past P)
             const int py = (p.by_contraction ? 0 : it.group * p.p_rows) + it.p0;
             const int half = it.nq / 2, boxes = (half + 31) / 32;               // pair: Q rows of each CTA, in boxes of 32
-            if (lane == 0) {
-                for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                    if ((n & 1) == pid) {
-                        if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ph ^ 1, kRoleTma)) break;
+            const bool whole = !kPair || it.nq == TQ;
+            const uint32_t bytes = kAStageBytes + (whole ? C::kQBytes : boxes * 32 * 128);
+            const int qy = it.q0 + (kPair ? rank * half : 0);
+            const uint8_t* sfp = p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) + (size_t)pa * 512;
+            const uint8_t* sfq = p.q_scale + (size_t)qa * 512;
+            for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+                if (turn == 0) {
+                    if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ph ^ 1, kRoleTma)) break;
+                    if (leader) {
                         uint8_t* pd = smem + (size_t)stage * C::kStageBytes;
                         uint8_t* qd = pd + kAStageBytes;
                         mbar_arrive_expect_tx(&ctl->sf_full[stage], 512 * (1 + atoms));
-                        bulk_load(smem + C::oSfp + stage * 512,
-                                  p.p_scale + (p.by_contraction ? 0 : (size_t)it.group * p.p_scale_group) +
-                                      ((size_t)kb * p.p_row_tiles + pa) * 512,
-                                  512, &ctl->sf_full[stage]);
-                        bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512,
-                                  p.q_scale + ((size_t)kb * p.q_row_tiles + qa) * 512, 512 * atoms, &ctl->sf_full[stage]);
+                        bulk_load(smem + C::oSfp + stage * 512, sfp + (size_t)kb * p.p_row_tiles * 512, 512, &ctl->sf_full[stage]);
+                        bulk_load(smem + C::oSfq + (size_t)stage * C::kQAtoms * 512, sfq + (size_t)kb * p.q_row_tiles * 512, 512 * atoms,
+                                  &ctl->sf_full[stage]);
                         if constexpr (kPair) {
-                            const bool whole = it.nq == TQ;
-                            const uint32_t bytes = kAStageBytes + (whole ? C::kQBytes : boxes * 32 * 128);
                             const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
                             if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
                             tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
-                            const int qy = it.q0 + rank * half;
                             if (whole)
                                 tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
                             else
                                 for (int b = 0; b < boxes; ++b)
                                     tma_load_2d_pair(qd + b * 4096, &map_q32, bar, kb * 128, qy + b * 32, keep);
                         } else {
-                            mbar_arrive_expect_tx(&ctl->full[stage], kAStageBytes + C::kQBytes);
+                            mbar_arrive_expect_tx(&ctl->full[stage], bytes);
                             tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
-                            tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, it.q0);
+                            tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, qy);
                         }
                         ctl->issued[pid] = n + 1;
                     }
-                    if (++stage == stages) {
-                        stage = 0;
-                        ph ^= 1;
-                    }
+                    __syncwarp();
+                    turn = kProd;
+                }
+                --turn;
+                if (++stage == stages) {
+                    stage = 0;
+                    ph ^= 1;
                 }
             }
             __syncwarp();
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // The whole warp walks the loop (the descriptors stay in uniform registers),
         // one elected lane issues.
         const bool leader = elect_one();
-        int stage = 0, acc = 0;
+        int stage = 0, slot = 0, acc = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
-                    const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
+                    const uint32_t sf = tmem + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     const int k0 = max(0, it.b0 - kb * 4), k1 = min(4, it.b1 - kb * 4);
@@ -590,6 +597,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                         stage = 0;
                         ph ^= 1;
                     }
+                    if (kPair && ++slot == C::kSfSlots) slot = 0;
                 }
                 if (leader) {
                     if constexpr (kPair)
@@ -606,16 +614,21 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // ---------------------------------------------------------- scale warps
         const int quarter = warp & 3;
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
-        int stage = 0;
+        int n = 0, stage = 0, slot = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
             const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
-            for (int kb = it.kb0; kb < it.kb1; ++kb) {
+            for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 lin_wait(p, ctl, &ctl->sf_full[stage], ph, kRoleScale);
+                if (kPair && n >= C::kSfSlots) {   // (fewer slots than stages: the slot's last MMAs are done)
+                    const int u = n - C::kSfSlots;
+                    lin_wait<kPair>(p, ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale);
+                }
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)stage * C::kSfCols;
+                const uint32_t t =
+                    tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
                 tmem_st_32x32b_x4(t, reinterpret_cast<const uint4*>(smem + C::oSfp + stage * 512)[lane]);
                 const uint8_t* sq = smem + C::oSfq + (size_t)stage * C::kQAtoms * 512;
                 // words 4 a + shift .. of the tiles' concatenated columns
@@ -647,6 +660,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     stage = 0;
                     ph ^= 1;
                 }
+                if (kPair && ++slot == C::kSfSlots) slot = 0;
             }
             __syncwarp();
             if (split) lin_tile_end(tile + stride < total);
@@ -785,8 +799,6 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 }
             }
         }
-    } else if (split) {
-        for (int tile = first; tile < total; tile += stride) lin_tile_end(tile + stride < total);
     }
     __syncthreads();
     if (ctl->abort && threadIdx.x == 0) {
@@ -794,12 +806,11 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // time to land (bounded) before the CTA ends (pair: the even CTA's
         // barrier counts both CTAs' loads, and both end together below)
         const uint64_t t0 = globaltimer();
-        for (int s = 0; s < stages; ++s) {
-            const int last = max(ctl->issued[0], ctl->issued[1]) - 1;
-            const int n = last - ((last - s) % stages + stages) % stages;   // stage s's last use
-            if (n < 0) continue;
-            while (!((kPair && rank != 0) || lin_try<kPair>(&ctl->full[s], (n / stages) & 1)) ||
-                   !mbar_try_wait(&ctl->sf_full[s], (n / stages) & 1))
+        const int last = max(max(ctl->issued[0], ctl->issued[1]), ctl->issued[2]) - 1;
+        for (int i = 0; i < 2 * stages; ++i) {   // operands, then scale tiles
+            const int s = i % stages, n = last - ((last - s) % stages + stages) % stages;   // stage s's last use
+            if (n < 0 || (i < stages && kPair && rank != 0)) continue;
+            while (!lin_try<kPair>(i < stages ? &ctl->full[s] : &ctl->sf_full[s], (n / stages) & 1))
                 if (globaltimer() - t0 > (uint64_t)p.timeout_ns) break;
         }
     }
