@@ -286,6 +286,34 @@ __device__ __forceinline__ void lin_store_bf16(uint16_t* out, int ld, const LinS
     }
 }
 
+// MXFP8 output: the warp's 32 features are one block of every token.
+template <int NC, bool kE5m2>
+__device__ __forceinline__ void lin_store_mx(const LinParams& p, const LinShare& e, int j0, int lane, const float (&v)[NC]) {
+    const int ld = p.p_rows, kb = e.f >> 7, i3 = lane & 3;
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (e.row + j0 + i3) * ld + (e.f & ~3);
+#pragma unroll
+    for (int j = 0; j < NC; j += 4, o += 4 * (size_t)ld) {
+        float s[4];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t byte =
+                mx_scale_byte(__reduce_max_sync(kLanes, __float_as_uint(v[j + i]) & 0x7fffffffu), mx_emax<kE5m2>());
+            s[i] = v[j + i] * mx_inv_scale(byte);
+            bytes |= byte << (8 * i);
+        }
+        uint32_t w = __byte_perm(fp8x2<kE5m2>(s[0], s[1]), fp8x2<kE5m2>(s[2], s[3]), 0x5410);
+        // 4 x 4 byte transpose over four lanes: lane 4 a + i then holds features 4 a .. 4 a + 3 of token j + i
+        w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 1), lane & 1 ? 0x3715 : 0x6240);
+        w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 2), lane & 2 ? 0x3276 : 0x5410);
+        if (j0 + j + i3 < e.end) {
+            *reinterpret_cast<uint32_t*>(o) = w;
+            if (lane < 4)
+                p.out_scale[scale_word(kb, e.row + j0 + j + i3, p.q_row_tiles) + ((e.f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i3));
+        }
+    }
+}
+
 // Finish columns j0 .. j0 + NC - 1 of the share: v[j] are their sums.
 template <int NC>
 __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e, int j0, int lane, float (&v)[NC]) {
@@ -343,34 +371,10 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
                 if (j0 + j < e.end) *o = v[j];
         }
     } else {
-        // the warp's 32 features are one MX block of every token
-        uint8_t* out = static_cast<uint8_t*>(p.out);
-        const bool e5m2 = p.out_type == kTypeE5M2;
-        const int emax = mx_emax(e5m2), kb = e.f >> 7, i3 = lane & 3;
-        uint8_t* o = out + (e.row + j0 + i3) * ld + (e.f & ~3);
-#pragma unroll
-        for (int j = 0; j < NC; j += 4, o += 4 * (size_t)ld) {
-            float s[4];
-            uint32_t bytes = 0, nan = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t byte = mx_scale_byte(__reduce_max_sync(kLanes, __float_as_uint(v[j + i]) & 0x7fffffffu), emax);
-                s[i] = v[j + i] * mx_inv_scale(byte);
-                if (byte == 255) nan |= 0x7fu << (8 * i);
-                bytes |= byte << (8 * i);
-            }
-            uint32_t w = fp8x2(s[0], s[1], e5m2) | fp8x2(s[2], s[3], e5m2) << 16;
-            // (a NaN block's codes are all NaN)
-            w = (w & ~((nan >> 6 & 0x01010101u) * 0xffu)) | nan;
-            // 4 x 4 byte transpose over four lanes: lane 4 a + i then holds features 4 a .. 4 a + 3 of token j + i
-            w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 1), lane & 1 ? 0x3715 : 0x6240);
-            w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 2), lane & 2 ? 0x3276 : 0x5410);
-            if (j0 + j + i3 < e.end) {
-                *reinterpret_cast<uint32_t*>(o) = w;
-                if (lane < 4)
-                    p.out_scale[scale_word(kb, e.row + j0 + j + i3, p.q_row_tiles) + ((e.f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i3));
-            }
-        }
+        if (p.out_type == kTypeE5M2)
+            lin_store_mx<NC, true>(p, e, j0, lane, v);
+        else
+            lin_store_mx<NC, false>(p, e, j0, lane, v);
     }
 }
 

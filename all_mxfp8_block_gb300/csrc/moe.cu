@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_dispatch_copy_kernel(MoeDispa
 }
 
 // MX: 8 elements a lane and vector, 4 lanes a scale block, 16 lanes a scale word.
-template <typename T>
+template <typename T, bool kE5m2>
 __global__ void __launch_bounds__(kRowThreads) moe_dispatch_mx_kernel(MoeDispatch a, unsigned row_ctas, int parts) {
     const int kbs = (int)((a.hidden + 127) / 128), rt = (int)((a.seg.rows + 127) / 128);
     grid_wait();
@@ -235,8 +235,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_dispatch_mx_kernel(MoeDispatc
     const int lane = threadIdx.x % 32;
     const int h0 = (int)((blockIdx.x - t * parts) * blockDim.x + threadIdx.x / 32 * 32) * 8 * kDispatchUnroll + lane * 8;
     const T* x = static_cast<const T*>(a.x) + t * a.ldx;
-    const bool e5m2 = a.out_type == kTypeE5M2;
-    const int emax = mx_emax(e5m2);
+    constexpr int emax = mx_emax<kE5m2>();
     float f[kDispatchUnroll][8];
 #pragma unroll
     for (int u = 0; u < kDispatchUnroll; ++u) {
@@ -251,14 +250,15 @@ __global__ void __launch_bounds__(kRowThreads) moe_dispatch_mx_kernel(MoeDispatc
     uint32_t word[kDispatchUnroll];
 #pragma unroll
     for (int u = 0; u < kDispatchUnroll; ++u) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[u][i]));
+        const float* x8 = f[u];
+        float m = abs_max(abs_max(0.f, x8[0], x8[1]), x8[2], x8[3]);
+        m = abs_max(abs_max(m, x8[4], x8[5]), x8[6], x8[7]);
         m = max_nan(m, __shfl_xor_sync(kLanes, m, 1));
         m = max_nan(m, __shfl_xor_sync(kLanes, m, 2));
         const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
         const float inv = mx_inv_scale(byte);
-        code[u] = make_uint2(mx_codes4(f[u], inv, byte == 255, e5m2), mx_codes4(f[u] + 4, inv, byte == 255, e5m2));
+        code[u] = make_uint2(mx_codes4<kE5m2>(make_float2(x8[0], x8[1]), make_float2(x8[2], x8[3]), inv),
+                             mx_codes4<kE5m2>(make_float2(x8[4], x8[5]), make_float2(x8[6], x8[7]), inv));
         // the four blocks' bytes of the 16-lane group into one word
         uint32_t w = byte << (8 * ((lane >> 2) & 3));
         w |= __shfl_xor_sync(kLanes, w, 4);
@@ -475,8 +475,8 @@ template <typename T>
 cudaError_t dispatch_mx(const MoeDispatch& a, cudaStream_t stream) {
     const RowShape r = row_shape(a.hidden, 256 * kDispatchUnroll);
     const unsigned ctas = (unsigned)(a.tokens * r.parts);
-    return launch(moe_dispatch_mx_kernel<T>, dim3(ctas + (unsigned)a.seg.experts * kPadParts), r.threads, 0, 1, stream, a, ctas,
-                  (int)r.parts);
+    return launch(a.out_type == kTypeE5M2 ? moe_dispatch_mx_kernel<T, true> : moe_dispatch_mx_kernel<T, false>,
+                  dim3(ctas + (unsigned)a.seg.experts * kPadParts), r.threads, 0, 1, stream, a, ctas, (int)r.parts);
 }
 
 template <typename T, int V>

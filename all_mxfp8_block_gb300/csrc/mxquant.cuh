@@ -114,18 +114,57 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, int emax) 
     const int e = (int)(amax_bits >> 23);   // 0 for zero and for subnormals, which clamp to -127 as well
     return e == 255 ? 255u : (uint32_t)max(e - emax, 0);
 }
-// 2^-X of a scale byte X + 127: always a normal number (X >= -127, X <= 119)
-__device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^-X of a scale byte X + 127: a normal number (X >= -127, X <= 119), NaN for byte 255
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) {
+    return __uint_as_float(byte == 255 ? 0x7fffffffu : (254u - byte) << 23);
+}
 
-// two codes, lo in the low byte (saturating, nearest even); nan: both NaN codes
-__device__ __forceinline__ uint32_t fp8x2(float lo, float hi, bool e5m2) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+// max(m, |a|, |b|), keeping a NaN: one instruction
+__device__ __forceinline__ float abs_max(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ uint32_t mx_codes4(const float* v, float inv, bool bad, bool e5m2) {
-    if (bad) return 0x7f7f7f7fu;   // NaN in both formats
-    return fp8x2(v[0] * inv, v[1] * inv, e5m2) | fp8x2(v[2] * inv, v[3] * inv, e5m2) << 16;
+// two fp32 operations in one instruction, each rounded as the single one
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return r;
 }
-__device__ __forceinline__ int mx_emax(bool e5m2) { return e5m2 ? 15 : 8; }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+          "l"(reinterpret_cast<const uint64_t&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// two codes, lo in the low byte (saturating, nearest even)
+template <bool kE5m2>
+__device__ __forceinline__ uint32_t fp8x2(float lo, float hi) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, kE5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+// four codes of v / 2^X (inv = 2^-X; a block with a NaN scale passes inv = NaN,
+// which makes all its codes NaN, 0x7f in both formats)
+template <bool kE5m2>
+__device__ __forceinline__ uint32_t mx_codes4(float2 a, float2 b, float inv) {
+    a = mul2(a, both(inv));
+    b = mul2(b, both(inv));
+    return __byte_perm(fp8x2<kE5m2>(a.x, a.y), fp8x2<kE5m2>(b.x, b.y), 0x5410);
+}
+template <bool kE5m2>
+__device__ constexpr int mx_emax() { return kE5m2 ? 15 : 8; }
 
 // byte offset of the scale word (4 scales: 128 elements along the contraction)
 // of row r, contraction block kb of 128, among rt row tiles of 128 rows
@@ -155,11 +194,17 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // roundings of its own size (ex2 and reciprocal approximations of 2^-22).
 //   gelu(z) = 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
 // The logistic's argument is kept where e is finite, i.e. z >= -87 (silu) or
-// |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35.
+// |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35
+// (silu's slope has no upper limit: e is 0 there).
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluA = 2.f * 0.7978845608028654f, kGeluB = 0.044715f;   // 2 sqrt(2 / pi)
-__device__ __forceinline__ float logistic_e(float e) { return __fdividef(1.f, 1.f + e); }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float logistic_e(float e) { return rcp_approx(1.f + e); }
 template <int kAct>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (kAct == kActRelu) {
@@ -174,20 +219,25 @@ __device__ __forceinline__ float act_value(float z) {
     }
     return z;
 }
+// g * act'(z) for two values at a time
 template <int kAct>
-__device__ __forceinline__ float act_slope(float z) {
+__device__ __forceinline__ float2 act_back2(float2 g, float2 z) {
     if constexpr (kAct == kActRelu) {
-        return z > 0.f ? 1.f : (z != z ? z : 0.f);
+        return make_float2(z.x > 0.f ? g.x : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? g.y : (z.y != z.y ? z.y : 0.f));
     } else if constexpr (kAct == kActSilu) {
-        const float m = min_nan(max_nan(z, -87.f), 87.f);
-        const float e = exp2f_approx(-kLog2e * m), s = logistic_e(e);
-        return fmaf(m * s, s * e, s);
+        const float2 m = make_float2(max_nan(z.x, -87.f), max_nan(z.y, -87.f)), x = mul2(m, both(-kLog2e));
+        const float2 e = make_float2(exp2f_approx(x.x), exp2f_approx(x.y)), d = add2(e, both(1.f));
+        const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        return mul2(g, fma2(mul2(m, s), mul2(s, e), s));
     } else if constexpr (kAct == kActGelu) {
-        const float m = min_nan(max_nan(z, -10.f), 10.f), m2 = m * m;
-        const float e = exp2f_approx(m * fmaf(kGeluA * kGeluB * -kLog2e, m2, kGeluA * -kLog2e)), s = logistic_e(e);
-        return fmaf(m * s * (s * e), fmaf(3.f * kGeluA * kGeluB, m2, kGeluA), s);
+        const float2 m = make_float2(min_nan(max_nan(z.x, -10.f), 10.f), min_nan(max_nan(z.y, -10.f), 10.f)), m2 = mul2(m, m);
+        const float2 x = mul2(m, fma2(m2, both(kGeluA * kGeluB * -kLog2e), both(kGeluA * -kLog2e)));
+        const float2 e = make_float2(exp2f_approx(x.x), exp2f_approx(x.y)), d = add2(e, both(1.f));
+        const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 w = fma2(m2, both(3.f * kGeluA * kGeluB), both(kGeluA));
+        return mul2(g, fma2(mul2(mul2(m, s), mul2(s, e)), w, s));
     }
-    return 1.f;
+    return g;
 }
 
 }  // namespace mxa2a

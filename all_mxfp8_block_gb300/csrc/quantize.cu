@@ -33,9 +33,7 @@ __device__ __forceinline__ bool row_is_token(const Segments& s, long long r) {
     return r >= o && r < o + s.counts[lo];
 }
 
-__device__ __forceinline__ float abs_max(float m, float v) { return max_nan(m, fabsf(v)); }
-
-template <typename T, int kAct>
+template <typename T, int kAct, bool kE5m2>
 __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int row_tiles) {
     __shared__ float4 tile[kTileRows * (kTileCols / 4)];
     __shared__ uint8_t token[kTileRows];
@@ -43,8 +41,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     const long long r0 = (long long)(blockIdx.x % row_tiles) * kTileRows;
     const int c0 = (int)blockIdx.y * kTileCols;
     const int tx = threadIdx.x % (kTileCols / 8), ty = threadIdx.x / (kTileCols / 8);
-    const bool e5m2 = q.e5m2;
-    const int emax = mx_emax(e5m2);
+    constexpr int emax = mx_emax<kE5m2>();
     const bool masked = q.seg.offsets != nullptr;
     grid_wait();
     grid_launch_next();
@@ -58,7 +55,9 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     const int rt = (int)((q.rows + 127) / 128), kb = c0 >> 7;
     const int col = c0 + tx * 8;
     const bool in_cols = col < q.cols;   // (columns come in blocks of 32)
-    float v[kPass][8];
+    float2 v[kPass][4];
+    typename Vec<T, 8>::Raw raw[kPass];
+    uint4 zw[kPass];
     bool live[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
@@ -66,24 +65,25 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
         const long long r = r0 + i;
         live[p] = in_cols && r < q.rows && (!masked || token[i]);
         if (live[p]) {
-            Vec<T, 8>::load(x + r * q.ldx + col, v[p]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[p][j] = 0.f;
+            raw[p] = Vec<T, 8>::raw(x + r * q.ldx + col);
+            if (kAct != kActNone) zw[p] = ptx::ld_nc_v4(static_cast<const __nv_bfloat16*>(q.preact) + r * q.cols + col);
         }
     }
-    if constexpr (kAct != kActNone) {
-        uint4 zw[kPass];
 #pragma unroll
-        for (int p = 0; p < kPass; ++p)
-            zw[p] = live[p] ? ptx::ld_nc_v4(static_cast<const __nv_bfloat16*>(q.preact) + (r0 + ty + p * 32) * q.cols + col)
-                            : make_uint4(0, 0, 0, 0);
+    for (int p = 0; p < kPass; ++p) {
+        float f[8];
+        Vec<T, 8>::values(raw[p], f);
 #pragma unroll
-        for (int p = 0; p < kPass; ++p) {
+        for (int j = 0; j < 4; ++j) v[p][j] = make_float2(f[2 * j], f[2 * j + 1]);
+        if constexpr (kAct != kActNone) {
             float z[8];
             Vec<__nv_bfloat16, 8>::unpack(&zw[p], z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[p][j] *= act_slope<kAct>(z[j]);
+            for (int j = 0; j < 4; ++j) v[p][j] = act_back2<kAct>(v[p][j], make_float2(z[2 * j], z[2 * j + 1]));
+        }
+        if (!live[p]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[p][j] = make_float2(0.f, 0.f);
         }
     }
     if (q.codes) {
@@ -94,12 +94,12 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
             const long long r = r0 + ty + p * 32;
             float m = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = abs_max(m, v[p][j]);
+            for (int j = 0; j < 4; ++j) m = abs_max(m, v[p][j].x, v[p][j].y);
             m = max_nan(m, __shfl_xor_sync(kLanes, m, 1));
             m = max_nan(m, __shfl_xor_sync(kLanes, m, 2));
             const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
             const float inv = mx_inv_scale(byte);
-            const uint2 w = make_uint2(mx_codes4(v[p], inv, byte == 255, e5m2), mx_codes4(v[p] + 4, inv, byte == 255, e5m2));
+            const uint2 w = make_uint2(mx_codes4<kE5m2>(v[p][0], v[p][1], inv), mx_codes4<kE5m2>(v[p][2], v[p][3], inv));
             if (in_cols && r < q.rows) *reinterpret_cast<uint2*>(codes + r * q.cols + col) = w;
             // two blocks of the tile's row in one 16-bit store (a tile is half a scale word wide)
             const uint32_t other = __shfl_xor_sync(kLanes, byte, 4);
@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     for (int p = 0; p < kPass; ++p) {
         // (the upper four threads of a row swap the order of their halves: no bank conflicts)
         float4* t = tile + (ty + p * 32) * (kTileCols / 4) + tx * 2;
-        const float4 lo = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]), hi = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
+        const float4 lo = make_float4(v[p][0].x, v[p][0].y, v[p][1].x, v[p][1].y);
+        const float4 hi = make_float4(v[p][2].x, v[p][2].y, v[p][3].x, v[p][3].y);
         const int swap = tx >> 2;
         t[swap] = swap ? hi : lo;
         t[swap ^ 1] = swap ? lo : hi;
@@ -126,20 +127,15 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     const long long t0 = r0 + rb * 32;
     const int ct = (int)((q.cols + 127) / 128), c = c0 + c4 * 4;
     const bool in_c = c < q.cols;
-    float u[8][4], m[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 u[8];
+    float2 s01 = make_float2(0.f, 0.f), s23 = s01;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float4 f = tile[(rb * 32 + rg * 8 + i) * (kTileCols / 4) + c4];
-        u[i][0] = f.x;
-        u[i][1] = f.y;
-        u[i][2] = f.z;
-        u[i][3] = f.w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = abs_max(m[j], u[i][j]);
-            sum[j] += u[i][j];
-        }
+        u[i] = tile[(rb * 32 + rg * 8 + i) * (kTileCols / 4) + c4];
+        s01 = add2(s01, make_float2(u[i].x, u[i].y));
+        s23 = add2(s23, make_float2(u[i].z, u[i].w));
     }
+    float sum[4] = {s01.x, s01.y, s23.x, s23.y};
     if (q.colsum) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -154,14 +150,19 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     uint8_t* scale_t = q.scale_t + (size_t)g * rt * ct * 512;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        m[j] = max_nan(m[j], __shfl_xor_sync(kLanes, m[j], 8));
-        m[j] = max_nan(m[j], __shfl_xor_sync(kLanes, m[j], 16));
-        const uint32_t byte = mx_scale_byte(__float_as_uint(m[j]), emax);
+        float w[8], m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = j == 0 ? u[i].x : j == 1 ? u[i].y : j == 2 ? u[i].z : u[i].w;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) m = abs_max(m, w[i], w[i + 1]);
+        m = max_nan(m, __shfl_xor_sync(kLanes, m, 8));
+        m = max_nan(m, __shfl_xor_sync(kLanes, m, 16));
+        const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
         const float inv = mx_inv_scale(byte);
-        const float a[4] = {u[0][j], u[1][j], u[2][j], u[3][j]}, b[4] = {u[4][j], u[5][j], u[6][j], u[7][j]};
         if (in_c && t0 < ld_t)
             *reinterpret_cast<uint2*>(q.codes_t + ((long long)g * q.cols + c + j) * ld_t + t0 + rg * 8) =
-                make_uint2(mx_codes4(a, inv, byte == 255, e5m2), mx_codes4(b, inv, byte == 255, e5m2));
+                make_uint2(mx_codes4<kE5m2>(make_float2(w[0], w[1]), make_float2(w[2], w[3]), inv),
+                           mx_codes4<kE5m2>(make_float2(w[4], w[5]), make_float2(w[6], w[7]), inv));
         if (in_c && rg == 0) scale_t[scale_word((int)(r0 >> 7), c + j, ct) + rb] = t0 < ld_t ? (uint8_t)byte : 0;
     }
     // the words of the last scale tile past the last column
@@ -211,22 +212,26 @@ __global__ void scale_tiles_kernel(const uint8_t* s, int groups, long long rows,
     }
 }
 
+template <typename T, int kAct, bool kE5m2>
+cudaError_t launch_one(const Quantize& q, dim3 grid, int row_tiles, cudaStream_t stream) {
+    return launch(quantize_kernel<T, kAct, kE5m2>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+}
+template <bool kE5m2>
+cudaError_t launch_format(const Quantize& q, dim3 grid, int row_tiles, cudaStream_t stream) {
+    if (q.x_type == kTypeF16) return launch_one<__half, kActNone, kE5m2>(q, grid, row_tiles, stream);
+    if (q.x_type == kTypeF32) return launch_one<float, kActNone, kE5m2>(q, grid, row_tiles, stream);
+    if (!q.preact) return launch_one<__nv_bfloat16, kActNone, kE5m2>(q, grid, row_tiles, stream);
+    if (q.act == kActRelu) return launch_one<__nv_bfloat16, kActRelu, kE5m2>(q, grid, row_tiles, stream);
+    if (q.act == kActGelu) return launch_one<__nv_bfloat16, kActGelu, kE5m2>(q, grid, row_tiles, stream);
+    return launch_one<__nv_bfloat16, kActSilu, kE5m2>(q, grid, row_tiles, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_quantize(const Quantize& q, cudaStream_t stream) {
     const int row_tiles = (int)((q.rows + kTileRows - 1) / kTileRows);
     const dim3 grid((unsigned)((long long)row_tiles * q.groups), (unsigned)((q.cols + kTileCols - 1) / kTileCols));
-    if (q.x_type == kTypeF16)
-        return launch(quantize_kernel<__half, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
-    if (q.x_type == kTypeF32)
-        return launch(quantize_kernel<float, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
-    if (!q.preact)
-        return launch(quantize_kernel<__nv_bfloat16, kActNone>, grid, kQThreads, 0, 1, stream, q, row_tiles);
-    if (q.act == kActRelu)
-        return launch(quantize_kernel<__nv_bfloat16, kActRelu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
-    if (q.act == kActGelu)
-        return launch(quantize_kernel<__nv_bfloat16, kActGelu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
-    return launch(quantize_kernel<__nv_bfloat16, kActSilu>, grid, kQThreads, 0, 1, stream, q, row_tiles);
+    return q.e5m2 ? launch_format<true>(q, grid, row_tiles, stream) : launch_format<false>(q, grid, row_tiles, stream);
 }
 
 cudaError_t launch_bias_sums(const float* colsum, const Segments& seg, long long cols, float* dbias, cudaStream_t stream) {
