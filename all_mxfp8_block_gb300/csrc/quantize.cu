@@ -37,9 +37,10 @@ template <typename T, int kAct, bool kE5m2>
 __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int row_tiles) {
     __shared__ float4 tile[kTileRows * (kTileCols / 4)];
     __shared__ uint8_t token[kTileRows];
-    const int g = (int)(blockIdx.x / row_tiles);
-    const long long r0 = (long long)(blockIdx.x % row_tiles) * kTileRows;
-    const int c0 = (int)blockIdx.y * kTileCols;
+    const int g = (int)(blockIdx.x / row_tiles), row_tile = (int)blockIdx.x - g * row_tiles;
+    const long long r0 = (long long)row_tile * kTileRows;
+    const int left = (int)min((long long)kTileRows, q.rows - r0);   // rows of the tile
+    const int cols = (int)q.cols, c0 = (int)blockIdx.y * kTileCols, ct = (cols + 127) >> 7;
     const int tx = threadIdx.x % (kTileCols / 8), ty = threadIdx.x / (kTileCols / 8);
     constexpr int emax = mx_emax<kE5m2>();
     const bool masked = q.seg.offsets != nullptr;
@@ -47,26 +48,26 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     grid_launch_next();
     if (masked) {
         if (r0 >= q.seg.offsets[q.seg.experts]) return;   // past the last segment: nothing is read from there
-        if (threadIdx.x < kTileRows)
-            token[threadIdx.x] = r0 + threadIdx.x < q.rows && row_is_token(q.seg, r0 + threadIdx.x);
+        if (threadIdx.x < kTileRows) token[threadIdx.x] = (int)threadIdx.x < left && row_is_token(q.seg, r0 + threadIdx.x);
         __syncthreads();
     }
-    const T* x = static_cast<const T*>(q.x) + (long long)g * q.rows * q.ldx;
-    const int rt = (int)((q.rows + 127) / 128), kb = c0 >> 7;
+    // (addresses once per thread; a pass is 32 rows further)
     const int col = c0 + tx * 8;
-    const bool in_cols = col < q.cols;   // (columns come in blocks of 32)
+    const bool in_cols = col < cols;   // (columns come in blocks of 32)
+    const long long row = (long long)g * q.rows + r0 + ty;
+    const T* x = static_cast<const T*>(q.x) + row * q.ldx + col;
+    const __nv_bfloat16* pre = static_cast<const __nv_bfloat16*>(q.preact) + row * cols + col;
+    const long long x_pass = 32 * q.ldx, c_pass = 32ll * cols;
     float2 v[kPass][4];
     typename Vec<T, 8>::Raw raw[kPass];
     uint4 zw[kPass];
     bool live[kPass];
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-        const int i = ty + p * 32;
-        const long long r = r0 + i;
-        live[p] = in_cols && r < q.rows && (!masked || token[i]);
+        live[p] = in_cols && ty + p * 32 < left && (!masked || token[ty + p * 32]);
         if (live[p]) {
-            raw[p] = Vec<T, 8>::raw(x + r * q.ldx + col);
-            if (kAct != kActNone) zw[p] = ptx::ld_nc_v4(static_cast<const __nv_bfloat16*>(q.preact) + r * q.cols + col);
+            raw[p] = Vec<T, 8>::raw(x + p * x_pass);
+            if (kAct != kActNone) zw[p] = ptx::ld_nc_v4(pre + p * c_pass);
         }
     }
 #pragma unroll
@@ -87,11 +88,10 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
         }
     }
     if (q.codes) {
-        uint8_t* codes = q.codes + (long long)g * q.rows * q.cols;
-        uint8_t* scale = q.scale + (size_t)g * ((q.cols + 127) / 128) * rt * 512;
+        uint8_t* codes = q.codes + row * cols + col;
+        uint8_t* scale = q.scale + (((size_t)g * ct + (c0 >> 7)) * row_tiles + row_tile) * 512 + ty * 16 + ((c0 >> 5) & 3);
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
-            const long long r = r0 + ty + p * 32;
             float m = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) m = abs_max(m, v[p][j].x, v[p][j].y);
@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
             const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
             const float inv = mx_inv_scale(byte);
             const uint2 w = make_uint2(mx_codes4<kE5m2>(v[p][0], v[p][1], inv), mx_codes4<kE5m2>(v[p][2], v[p][3], inv));
-            if (in_cols && r < q.rows) *reinterpret_cast<uint2*>(codes + r * q.cols + col) = w;
+            if (in_cols && ty + p * 32 < left) *reinterpret_cast<uint2*>(codes + p * c_pass) = w;
             // two blocks of the tile's row in one 16-bit store (a tile is half a scale word wide)
             const uint32_t other = __shfl_xor_sync(kLanes, byte, 4);
             if (tx == 0) {   // (rows past the last and blocks past the last column get scale 0: every byte is written)
-                uint16_t* s = reinterpret_cast<uint16_t*>(scale + scale_word(kb, r, rt) + ((c0 >> 5) & 3));
-                s[0] = (uint16_t)(byte | (c0 + 32 < q.cols ? other : 0u) << 8);
-                if (c0 + kTileCols >= q.cols && (c0 & 64) == 0) s[1] = 0;
+                uint16_t* s = reinterpret_cast<uint16_t*>(scale + p * 4);
+                s[0] = (uint16_t)(byte | (c0 + 32 < cols ? other : 0u) << 8);
+                if (c0 + kTileCols >= cols && (c0 & 64) == 0) s[1] = 0;
             }
         }
     }
@@ -124,9 +124,8 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     __syncthreads();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int c4 = (lane & 7) + 8 * (warp & 1), rg = lane >> 3, rb = warp >> 1;   // 4 columns; 8 of the 32 rows of block rb
-    const long long t0 = r0 + rb * 32;
-    const int ct = (int)((q.cols + 127) / 128), c = c0 + c4 * 4;
-    const bool in_c = c < q.cols;
+    const int c = c0 + c4 * 4;
+    const bool in_c = c < cols, in_t = in_c && rb * 32 < left;   // (rows past the last inside a block of 32 are zeros)
     float4 u[8];
     float2 s01 = make_float2(0.f, 0.f), s23 = s01;
 #pragma unroll
@@ -142,12 +141,15 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
             sum[j] += __shfl_xor_sync(kLanes, sum[j], 8);
             sum[j] += __shfl_xor_sync(kLanes, sum[j], 16);
         }
-        if (rg == 0 && in_c && t0 < q.rows)
-            *reinterpret_cast<float4*>(q.colsum + (t0 >> 5) * q.cols + c) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        if (rg == 0 && in_t)
+            *reinterpret_cast<float4*>(q.colsum + (long long)(row_tile * 4 + rb) * cols + c) = make_float4(sum[0], sum[1], sum[2], sum[3]);
     }
     if (!q.codes_t) return;
     const long long ld_t = (q.rows + 31) / 32 * 32;
-    uint8_t* scale_t = q.scale_t + (size_t)g * rt * ct * 512;
+    uint8_t* codes_t = q.codes_t + ((long long)g * cols + c) * ld_t + r0 + rb * 32 + rg * 8;
+    // (a thread's 4 columns are neighbours in one 32-row group of their scale tile)
+    uint8_t* scale_t = q.scale_t + ((size_t)g * row_tiles + row_tile) * ct * 512;
+    uint8_t* word = scale_t + (size_t)(c >> 7) * 512 + (c & 31) * 16 + ((c & 127) >> 5) * 4 + rb;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float w[8], m = 0.f;
@@ -159,16 +161,16 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
         m = max_nan(m, __shfl_xor_sync(kLanes, m, 16));
         const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
         const float inv = mx_inv_scale(byte);
-        if (in_c && t0 < ld_t)
-            *reinterpret_cast<uint2*>(q.codes_t + ((long long)g * q.cols + c + j) * ld_t + t0 + rg * 8) =
+        if (in_t)
+            *reinterpret_cast<uint2*>(codes_t + j * ld_t) =
                 make_uint2(mx_codes4<kE5m2>(make_float2(w[0], w[1]), make_float2(w[2], w[3]), inv),
                            mx_codes4<kE5m2>(make_float2(w[4], w[5]), make_float2(w[6], w[7]), inv));
-        if (in_c && rg == 0) scale_t[scale_word((int)(r0 >> 7), c + j, ct) + rb] = t0 < ld_t ? (uint8_t)byte : 0;
+        if (in_c && rg == 0) word[j * 16] = in_t ? (uint8_t)byte : 0;
     }
     // the words of the last scale tile past the last column
-    if (c0 + kTileCols >= q.cols)
-        for (int i = (int)q.cols + threadIdx.x; i < ct * 128; i += kQThreads)
-            *reinterpret_cast<uint32_t*>(scale_t + scale_word((int)(r0 >> 7), i, ct)) = 0;
+    if (c0 + kTileCols >= cols)
+        for (int i = cols + threadIdx.x; i < ct * 128; i += kQThreads)
+            *reinterpret_cast<uint32_t*>(scale_t + (size_t)(i >> 7) * 512 + (i & 31) * 16 + ((i & 127) >> 5) * 4) = 0;
 }
 
 // dbias: the 32-row blocks' column sums of a segment, added in order: a CTA
