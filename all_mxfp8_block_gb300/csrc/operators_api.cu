@@ -301,27 +301,32 @@ int layer_device(const mxa2a_linear* l) {
 }
 
 // Tile width, contraction split and grid of one product.
-// tokens: about how many Q rows a group has; tiles(tq): tiles of the launch, at most.
-// * The tile is the narrowest that holds a group's rows with a fifth to spare:
-//   columns past a group's last row are multiplied for nothing, and a wider
-//   tile re-reads the P rows less often.
+// rows: Q rows that a tile should hold; tiles(tq): tiles of the launch, at most.
+// * The tile is the narrowest that holds a group's rows: columns past a group's
+//   last row are multiplied for nothing, and a wider tile re-reads the P rows
+//   less often.
+// * Rows for 256-wide tiles go to the CTA-pair kernel once its tiles fill half
+//   of the pairs (1024 x 4096 x 4096, 64 tiles: 19.8 us against 21.9 us on single
+//   CTAs; 512 x 4096 x 4096, 32 tiles: 18.1 against 13.9), else to single CTAs on
+//   128-wide tiles.
 // * A launch with fewer tiles than CTAs splits the contraction over a cluster,
-//   as far as every part keeps two 128-wide blocks.
+//   as far as every part keeps two 128-wide blocks (1 token x 7168 x 8192, 56
+//   tiles: 20.3, 17.0, 23.0 us for 2, 4, 8 parts; 8 parts no longer fit at once).
 struct Shape {
     int tq, splits, ctas;
 };
 template <typename Tiles>
-Shape choose_shape(int sms, double tokens, int kblocks, Tiles tiles) {
+Shape choose_shape(int sms, double rows, int kblocks, Tiles tiles) {
     Shape s;
-    s.tq = tokens * 1.2 <= 32 ? 32 : tokens * 1.2 <= 64 ? 64 : tokens * 1.2 <= 128 ? 128 : 256;
+    s.tq = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     if (s.tq == 256) {
         s.splits = 1;
         const int64_t pairs = std::min<int64_t>(tiles(256), sms / 2);
-        if (pairs == sms / 2) {
+        if (pairs * 2 >= sms / 2) {
             s.ctas = (int)pairs * 2;
             return s;
         }
-        s.tq = 128;   // fewer pair tiles than pairs: single CTAs on narrower tiles
+        s.tq = 128;
     }
     const int64_t slots = (int64_t)sms * linear_ctas_per_sm(s.tq), n = std::max<int64_t>(1, tiles(s.tq));
     s.splits = 1;
@@ -336,7 +341,7 @@ struct Product {
     int64_t p_groups;                    // matrices behind p
     int by_contraction;
     int groups;
-    double tokens;
+    double tile_rows;                    // Q rows that a tile should hold
 };
 
 int launch_product(mxa2a_linear* l, const Product& d, LinParams p, cudaStream_t stream) {
@@ -355,7 +360,7 @@ int launch_product(mxa2a_linear* l, const Product& d, LinParams p, cudaStream_t 
     const int kblocks = (int)((d.cols + 127) / 128);
     const int64_t groups = d.groups, q = d.q_rows;
     const bool by_c = d.by_contraction != 0, segs = p.offsets != nullptr;
-    const Shape s = choose_shape(l->sms, d.tokens, by_c ? std::max<int>(1, (int)(kblocks / groups)) : kblocks, [&](int tq) {
+    const Shape s = choose_shape(l->sms, d.tile_rows, by_c ? std::max<int>(1, (int)(kblocks / groups)) : kblocks, [&](int tq) {
         const int64_t whole = (q + tq - 1) / tq, pt = (d.p_rows + linear_p_tile(tq) - 1) / linear_p_tile(tq);
         if (by_c) return groups * pt * whole;
         // (a group's last tile may be partly filled; a group without rows has none)
@@ -375,11 +380,13 @@ int launch_product(mxa2a_linear* l, const Product& d, LinParams p, cudaStream_t 
     return cuda_code(launch_linear(p, s.tq, mp, mq, mq32, s.ctas, stream));
 }
 
-// tokens of a group, from the row capacity that the caller gave: every segment may hold up to 31 rows of padding
-double tokens_per_group(int64_t rows, int groups, bool segs) {
+// Rows of a tile: all of them without segments; else a group's mean and a fifth
+// to spare, from the row capacity that the caller gave, in which every segment
+// may hold up to 31 rows of padding.
+double rows_per_group(int64_t rows, int groups, bool segs) {
     if (!segs) return (double)rows;
     const int64_t least = std::max<int64_t>(rows - 31ll * groups, rows / 32);
-    return (double)least / groups;
+    return 1.2 * (double)least / groups;
 }
 
 }  // namespace
@@ -417,7 +424,7 @@ int mxa2a_linear_run(mxa2a_linear* l, int64_t rows, const void* x, const void* x
     p.out_type = out_type;
     p.out_scale = static_cast<uint8_t*>(out_scale);
     const Product d = {w, w_scale, x, x_scale, l->N, rows, l->K, l->groups, 0, l->groups,
-                       tokens_per_group(rows, l->groups, offsets != nullptr)};
+                       rows_per_group(rows, l->groups, offsets != nullptr)};
     return launch_product(l, d, p, static_cast<cudaStream_t>(stream));
 }
 
@@ -486,7 +493,7 @@ int mxa2a_linear_backward(mxa2a_linear* l, int64_t rows, const void* dy, const v
         p.out = dx;
         p.out_type = kTypeBf16;
         const Product d = {w_t, w_t_scale, l->dz, l->dz_scale, l->K, rows, l->N, l->groups, 0, l->groups,
-                           tokens_per_group(rows, l->groups, offsets != nullptr)};
+                           rows_per_group(rows, l->groups, offsets != nullptr)};
         if (int rc = launch_product(l, d, p, st)) return rc;
     }
     if (dw) {
