@@ -287,31 +287,41 @@ __device__ __forceinline__ void lin_store_bf16(uint16_t* out, int ld, const LinS
     }
 }
 
-// MXFP8 output: the warp's 32 features are one block of every token.
+// max |v| over the warp's lanes, keeping a NaN
+__device__ __forceinline__ float lin_warp_amax(float v) {
+    float r;
+    asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// MXFP8 output: the warp's 32 features are one block of every token.  The
+// blocks' largest values come as one reduction per column; lane j then works
+// out column j's scale byte and factor for all, and stores the byte.
 template <int NC, bool kE5m2>
 __device__ __forceinline__ void lin_store_mx(const LinParams& p, const LinShare& e, int j0, int lane, const float (&v)[NC]) {
-    const int ld = p.p_rows, kb = e.f >> 7, i3 = lane & 3;
+    const int ld = p.p_rows, i3 = lane & 3;
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        const float m = lin_warp_amax(v[j]);
+        if (lane == j) amax = m;
+    }
+    const uint32_t byte = mx_scale_byte(__float_as_uint(amax), mx_emax<kE5m2>());
+    const float inv = mx_inv_scale(byte);
+    if (lane < NC && j0 + lane < e.end)
+        p.out_scale[scale_word(e.f >> 7, e.row + j0 + lane, p.q_row_tiles) + ((e.f >> 5) & 3)] = (uint8_t)byte;
     uint8_t* o = static_cast<uint8_t*>(p.out) + (e.row + j0 + i3) * ld + (e.f & ~3);
+    const size_t step = 4 * (size_t)ld;
 #pragma unroll
-    for (int j = 0; j < NC; j += 4, o += 4 * (size_t)ld) {
+    for (int j = 0; j < NC; j += 4, o += step) {
         float s[4];
-        uint32_t bytes = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t byte =
-                mx_scale_byte(__reduce_max_sync(kLanes, __float_as_uint(v[j + i]) & 0x7fffffffu), mx_emax<kE5m2>());
-            s[i] = v[j + i] * mx_inv_scale(byte);
-            bytes |= byte << (8 * i);
-        }
+        for (int i = 0; i < 4; ++i) s[i] = v[j + i] * __shfl_sync(kLanes, inv, j + i);
         uint32_t w = __byte_perm(fp8x2<kE5m2>(s[0], s[1]), fp8x2<kE5m2>(s[2], s[3]), 0x5410);
         // 4 x 4 byte transpose over four lanes: lane 4 a + i then holds features 4 a .. 4 a + 3 of token j + i
         w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 1), lane & 1 ? 0x3715 : 0x6240);
         w = __byte_perm(w, __shfl_xor_sync(kLanes, w, 2), lane & 2 ? 0x3276 : 0x5410);
-        if (j0 + j + i3 < e.end) {
-            *reinterpret_cast<uint32_t*>(o) = w;
-            if (lane < 4)
-                p.out_scale[scale_word(kb, e.row + j0 + j + i3, p.q_row_tiles) + ((e.f >> 5) & 3)] = (uint8_t)(bytes >> (8 * i3));
-        }
+        if (j0 + j + i3 < e.end) *reinterpret_cast<uint32_t*>(o) = w;
     }
 }
 
@@ -376,6 +386,22 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
             lin_store_mx<NC, true>(p, e, j0, lane, v);
         else
             lin_store_mx<NC, false>(p, e, j0, lane, v);
+    }
+}
+
+// Zeros for a whole tile of the by-contraction output (BF16 or FP32): rows in
+// turn over the warps, 16 bytes a lane.
+template <int TQ>
+__device__ __forceinline__ void lin_store_zeros(const LinParams& p, const LinItem& it, int warp, int warps, int lane) {
+    const int size = p.out_type == kTypeF32 ? 4 : 2, units = min(128, p.p_rows - it.p0) * size / 16;   // (of 8 or 4 columns)
+    uint8_t* out = static_cast<uint8_t*>(p.out) + (((long long)it.group * p.q_rows + it.q0) * p.p_rows + it.p0) * size;
+    const int rows = it.q_end - it.q0;
+    if (size == 2) {   // two rows at a time
+        for (int r = 2 * warp + (lane >> 4); r < rows; r += 2 * warps)
+            if ((lane & 15) < units) reinterpret_cast<uint4*>(out + (long long)r * p.p_rows * 2)[lane & 15] = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int r = warp; r < rows; r += warps)
+            if (lane < units) reinterpret_cast<uint4*>(out + (long long)r * p.p_rows * 4)[lane] = make_uint4(0, 0, 0, 0);
     }
 }
 
@@ -702,6 +728,12 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 lin_wait<kPair>(p, ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
                 __syncwarp();
                 tc_fence_after();
+            }
+            if (p.by_contraction && it.b1 <= it.b0) {   // a group without tokens
+                const int warps = split ? C::kEpiWarps * p.splits : C::kEpiWarps;
+                lin_store_zeros<TQ>(p, it, (split ? rank * C::kEpiWarps : 0) + warp - 8, warps, lane);
+                if (split) lin_tile_end(tile + stride < total);
+                continue;
             }
             const LinShare e = lin_share(p, it, f, part * C::kColsPerWarp);
             if constexpr (kPair) {

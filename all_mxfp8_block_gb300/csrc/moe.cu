@@ -496,12 +496,17 @@ cudaError_t combine_t(const MoeCombine& a, cudaStream_t stream) {
     return combine_v<T, 1>(a, stream);
 }
 
+template <typename T, int V>
+cudaError_t combine_backward_v(const MoeCombineBackward& a, cudaStream_t stream) {
+    const dim3 ctas((unsigned)(a.tokens + (long long)a.seg.experts * kPadParts));
+    // as many warps to a token as its row has pieces, at most 8 (more CTAs to an SM for narrow rows)
+    return launch(moe_combine_backward_kernel<T, V>, ctas, row_shape(a.hidden, 32 * V).threads, 0, 1, stream, a);
+}
 template <typename T>
 cudaError_t combine_backward_t(const MoeCombineBackward& a, cudaStream_t stream) {
-    const dim3 ctas((unsigned)(a.tokens + (long long)a.seg.experts * kPadParts));
     if (aligned_rows<T>(a.y, a.hidden) && aligned_rows<T>(a.dy, a.hidden) && aligned_rows<T>(a.dout, a.hidden))
-        return launch(moe_combine_backward_kernel<T, 16 / sizeof(T)>, ctas, kRowThreads, 0, 1, stream, a);
-    return launch(moe_combine_backward_kernel<T, 1>, ctas, kRowThreads, 0, 1, stream, a);
+        return combine_backward_v<T, 16 / sizeof(T)>(a, stream);
+    return combine_backward_v<T, 1>(a, stream);
 }
 
 }  // namespace
