@@ -117,7 +117,7 @@ struct __align__(8) LinCtl {
 template <int TQ>
 constexpr size_t LinCfg<TQ>::ctl_bytes() { return oCtl + sizeof(LinCtl) + 1024; }
 
-__device__ __noinline__ void lin_report(const LinParams& p, int role, long long parity) {
+__device__ __forceinline__ void lin_report(const LinParams& p, int role, long long parity) {
     DevStatus* st = p.status;
     const unsigned long long mine = (p.launch_id << 8) | (unsigned long long)kErrTimeout;
     unsigned long long cur = atomicAdd(&st->key, 0ull);
@@ -332,7 +332,7 @@ __device__ __forceinline__ void lin_store(const LinParams& p, const LinShare& e,
     if (j0 >= e.end) return;   // (uniform over the warp)
     const int ld = p.p_rows;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) v[j] += e.bias;
+    for (int j = 0; j < NC; ++j) v[j] += e.bias;   // (0 without one: a branch here spills registers)
     if (j0 + NC > e.live) {
 #pragma unroll
         for (int j = 0; j < NC; ++j) v[j] = j0 + j < e.live ? v[j] : 0.f;
@@ -405,6 +405,13 @@ __device__ __forceinline__ void lin_store_zeros(const LinParams& p, const LinIte
     }
 }
 
+// The pair kernel's registers: its epilogue holds 64 columns beside the piece in
+// work; 8 warps x 192 + 8 x 64 are the launch's 16 x 128.  (No function calls in
+// that kernel: the split is then not allocated.)
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -524,6 +531,9 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 
     if (kPair || split) cluster_sync();   // every CTA of the cluster runs before any touches its shared memory
 
+    // (whole warpgroups take each side; each side's code follows its register count)
+    if (warp < 8) {
+    if constexpr (kPair) regs_down<64>();
     if (warp == 0 || (warp >= 2 && warp <= kProd)) {
         // ---------------------------------------------------------- TMA producers: the stages in turn
         const bool leader = elect_one();
@@ -710,8 +720,10 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             __syncwarp();
             if (split) lin_tile_end(tile + stride < total);
         }
-    } else if (warp >= 8) {
+    }
+    } else {
         // ---------------------------------------------------------- epilogue
+        if constexpr (kPair) regs_up<192>();
         const int quarter = warp & 3, part = (warp - 8) >> 2;
         // shared tiles: the others' parts of this CTA's columns, [splits - 1][TQ / splits][128] fp32
         const float* parts_in = reinterpret_cast<const float*>(smem + C::oPart);
@@ -740,13 +752,16 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                 // The 64 columns that the next tile's accumulator takes over (the
                 // tile's last in the first accumulator, its first in the second)
                 // go to registers first and are handed over; 32 columns at a time
-                // then come from there or from tensor memory.
+                // then come from there or from tensor memory (loading a piece while
+                // another is finished measured slower: 35.1 -> 41.3 us on 4096 x 8192
+                // x 512).
                 const int over = buf == 0 ? C::kColsPerWarp - C::kOverlap : 0;
                 const bool mine = live && part == (buf ^ 1);
+                constexpr int NC = 32;
                 float v[C::kOverlap];
                 if (mine) {
 #pragma unroll
-                    for (int i = 0; i < C::kOverlap; i += 32)
+                    for (int i = 0; i < C::kOverlap; i += NC)
                         tmem_ld_32x32b_x32(t + (uint32_t)(over + i), *reinterpret_cast<uint32_t(*)[32]>(v + i));
                     tc_wait_ld();
                     tc_fence_before();
@@ -759,21 +774,21 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     }
                 }
 #pragma unroll 1
-                for (int c = 0; c < C::kColsPerWarp; c += 32) {
-                    float u[32];
+                for (int c = 0; c < C::kColsPerWarp; c += NC) {
+                    float u[NC];
                     if (mine && c >= over && c < over + C::kOverlap) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) u[j] = v[j];
+                        for (int j = 0; j < NC; ++j) u[j] = v[j];
 #pragma unroll
-                        for (int j = 0; j < C::kOverlap - 32; ++j) v[j] = v[j + 32];
+                        for (int j = 0; j < C::kOverlap - NC; ++j) v[j] = v[j + NC];
                     } else if (live) {
                         tmem_ld_32x32b_x32(t + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(u));
                         tc_wait_ld();
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) u[j] = 0.f;
+                        for (int j = 0; j < NC; ++j) u[j] = 0.f;
                     }
-                    if (in_p) lin_store<32>(p, e, c, lane, u);
+                    if (in_p) lin_store<NC>(p, e, c, lane, u);
                 }
                 if (live) {
                     tc_fence_before();
