@@ -111,7 +111,7 @@ struct __align__(8) LinCtl {
     uint32_t tmem;
     volatile int abort;
     volatile int issued[3];           // stages issued by each producer
-    int total;                        // tiles of all groups
+    int total, rows_total;            // tiles of the launch; of its first product
     int start[kMaxGroups + 1];        // first tile of each group (grouped Q rows)
 };
 template <int TQ>
@@ -159,6 +159,7 @@ __device__ __forceinline__ bool lin_wait(const LinParams& p, LinCtl* ctl, uint64
 }
 
 struct LinItem {
+    int which;           // product of the launch
     int group;
     int p0;              // this CTA's first P row inside the group
     int q0;              // first Q row
@@ -174,9 +175,31 @@ __device__ __forceinline__ int seg_start(const LinParams& p, int g, int limit) {
     return max(0, min(*(p.offsets + g), limit)) & ~31;
 }
 
-template <int TQ>
-__device__ __forceinline__ LinItem lin_item(const LinParams& p, const LinCtl* ctl, int tile, int rank) {
+// a launch's one product, or its two
+struct LinOne {
+    static constexpr bool kTwo = false;
+    const LinParams& p0;
+    const CUtensorMap &mp, &mq, &mq32;
+    __device__ __forceinline__ const LinParams& p(int) const { return p0; }
+    __device__ __forceinline__ const CUtensorMap& map_p(int) const { return mp; }
+    __device__ __forceinline__ const CUtensorMap& map_q(int) const { return mq; }
+    __device__ __forceinline__ const CUtensorMap& map_q32(int) const { return mq32; }
+};
+struct LinTwo {
+    static constexpr bool kTwo = true;
+    const LinPack& k;
+    __device__ __forceinline__ const LinParams& p(int i) const { return k.p[i]; }
+    __device__ __forceinline__ const CUtensorMap& map_p(int i) const { return k.maps[i].p; }
+    __device__ __forceinline__ const CUtensorMap& map_q(int i) const { return k.maps[i].q; }
+    __device__ __forceinline__ const CUtensorMap& map_q32(int i) const { return k.maps[i].q32; }
+};
+
+template <int TQ, typename K>
+__device__ __forceinline__ LinItem lin_item(const K& k, const LinCtl* ctl, int tile, int rank) {
     LinItem it;
+    it.which = K::kTwo && tile >= ctl->rows_total ? 1 : 0;
+    if (it.which) tile -= ctl->rows_total;
+    const LinParams& p = k.p(it.which);
     int p_tile, q_tile, qt;
     if (p.by_contraction) {
         const int per = p.pt * p.qt;
@@ -437,19 +460,19 @@ __device__ __forceinline__ void lin_tile_end(bool more) {
     if (more) cluster_sync();
 }
 
-template <int TQ>
-__global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
-    linear_kernel(const __grid_constant__ LinParams p, const __grid_constant__ CUtensorMap map_p,
-                  const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q32) {
+// The launch's one product (LinOne) or two (LinTwo); kernels of their own, since
+// choosing a product per tile costs the pair kernel 3 %.
+template <int TQ, typename K>
+__device__ __forceinline__ void linear_body(const K& k) {
     using C = LinCfg<TQ>;
-    constexpr bool kPair = C::kPair;
+    constexpr bool kPair = C::kPair, kTwo = K::kTwo;
     extern __shared__ uint8_t lin_smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(lin_smem_raw) + 1023) & ~uintptr_t(1023));
     LinCtl* ctl = reinterpret_cast<LinCtl*>(smem + C::oCtl);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const bool split = !kPair && p.splits > 1;
+    const bool split = !kPair && k.p(0).splits > 1;
     const int stages = split ? C::kSplitStages : C::kStages;
-    const int share = kPair ? 2 : p.splits;      // CTAs to a tile
+    const int share = kPair ? 2 : k.p(0).splits;   // CTAs to a tile
     const int rank = kPair || split ? (int)cluster_ctarank() : 0;
     const int first = (int)blockIdx.x / share, stride = (int)gridDim.x / share;
 
@@ -468,8 +491,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         ctl->abort = 0;
         ctl->issued[0] = ctl->issued[1] = ctl->issued[2] = 0;
         fence_mbarrier_init();
-        prefetch_tensormap(&map_p);
-        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&k.map_p(0));
+        prefetch_tensormap(&k.map_q(0));
     }
     if (warp == 1) {
         if (kPair) {
@@ -480,33 +503,34 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             tmem_relinquish();
         }
     }
-    if (!kPair && threadIdx.x == 0 && !p.offsets && !p.by_contraction && p.q_rows <= TQ && first < p.pt) {
+    const LinParams& p0 = k.p(0);
+    if (!kPair && !kTwo && threadIdx.x == 0 && !p0.offsets && !p0.by_contraction && p0.q_rows <= TQ && first < p0.pt) {
         // One tile of Q rows (a decode step): the first weights on their way to L2
         // while the kernel before this one ends.  (A prefetch orders nothing and L2
         // holds what that kernel writes, so weights that it still writes are read
         // as written.)
-        const int hi = (p.blocks + 3) / 4, per = (hi + p.splits - 1) / p.splits, lo = rank * per;
-        for (int kb = lo; kb < min(min(hi, lo + per), lo + kEarly); ++kb) tma_prefetch_2d(&map_p, kb * 128, first * 128);
+        const int hi = (p0.blocks + 3) / 4, per = (hi + p0.splits - 1) / p0.splits, lo = rank * per;
+        for (int kb = lo; kb < min(min(hi, lo + per), lo + kEarly); ++kb) tma_prefetch_2d(&k.map_p(0), kb * 128, first * 128);
     }
     // (everything above touches this CTA's own memory only)
     grid_wait();
     if (warp == 3) {
-        // first tile of every group
-        if (p.by_contraction) {
-            if (lane == 0) ctl->total = p.groups * p.pt * p.qt;
+        // tiles of the launch; first tile of every group of Q rows
+        int sum = 0;
+        if (p0.by_contraction) {
+            sum = p0.groups * p0.pt * p0.qt;
         } else {
-            int carry = 0;
-            for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            for (int g0 = 0; g0 < p0.groups; g0 += 32) {
                 const int g = g0 + lane;
                 int n = 0;
-                if (g < p.groups) {
-                    int len = p.q_rows;
-                    if (p.offsets) {
-                        const int lo = seg_start(p, g, p.q_rows);
-                        const int hi = min(*(p.offsets + g + 1), p.q_rows);
+                if (g < p0.groups) {
+                    int len = p0.q_rows;
+                    if (p0.offsets) {
+                        const int lo = seg_start(p0, g, p0.q_rows);
+                        const int hi = min(*(p0.offsets + g + 1), p0.q_rows);
                         len = max(0, hi - lo);
                     }
-                    n = (len + TQ - 1) / TQ * p.pt;
+                    n = (len + TQ - 1) / TQ * p0.pt;
                 }
                 int inc = n;
 #pragma unroll
@@ -514,13 +538,14 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                     const int v = __shfl_up_sync(kLanes, inc, d);
                     if (lane >= d) inc += v;
                 }
-                if (g < p.groups) ctl->start[g] = carry + inc - n;
-                carry += __shfl_sync(kLanes, inc, 31);
+                if (g < p0.groups) ctl->start[g] = sum + inc - n;
+                sum += __shfl_sync(kLanes, inc, 31);
             }
-            if (lane == 0) {
-                ctl->start[p.groups] = carry;
-                ctl->total = carry;
-            }
+            if (lane == 0) ctl->start[p0.groups] = sum;
+        }
+        if (lane == 0) {
+            ctl->rows_total = sum;
+            ctl->total = sum + (kTwo ? k.p(1).groups * k.p(1).pt * k.p(1).qt : 0);
         }
     }
     __syncthreads();
@@ -546,7 +571,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
         const uint64_t keep = l2_policy_evict_last();
         for (int tile = first; tile < total; tile += stride) {
-            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
+            const LinParams& p = k.p(it.which);
             const int qa = it.q0 >> 7;                                          // first scale tile of the Q rows
             const int atoms = min(((it.q0 & 127) + TQ + 127) >> 7, p.q_row_tiles - qa);
             const int pa = min(it.p0 >> 7, p.p_row_tiles - 1);                  // (a pair's second half may lie past P)
@@ -559,7 +585,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             const uint8_t* sfq = p.q_scale + (size_t)qa * 512;
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
                 if (turn == 0) {
-                    if (!lin_wait<kPair>(p, ctl, &ctl->empty[stage], ph ^ 1, kRoleTma)) break;
+                    if (!lin_wait<kPair>(k.p(0), ctl, &ctl->empty[stage], ph ^ 1, kRoleTma)) break;
                     if (leader) {
                         uint8_t* pd = smem + (size_t)stage * C::kStageBytes;
                         uint8_t* qd = pd + kAStageBytes;
@@ -570,16 +596,16 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
                         if constexpr (kPair) {
                             const uint32_t bar = full0 + (uint32_t)stage * sizeof(uint64_t);
                             if (rank == 0) mbar_arrive_expect_tx(&ctl->full[stage], 2 * bytes);
-                            tma_load_2d_pair(pd, &map_p, bar, kb * 128, py, keep);
+                            tma_load_2d_pair(pd, &k.map_p(it.which), bar, kb * 128, py, keep);
                             if (whole)
-                                tma_load_2d_pair(qd, &map_q, bar, kb * 128, qy, keep);
+                                tma_load_2d_pair(qd, &k.map_q(it.which), bar, kb * 128, qy, keep);
                             else
                                 for (int b = 0; b < boxes; ++b)
-                                    tma_load_2d_pair(qd + b * 4096, &map_q32, bar, kb * 128, qy + b * 32, keep);
+                                    tma_load_2d_pair(qd + b * 4096, &k.map_q32(it.which), bar, kb * 128, qy + b * 32, keep);
                         } else {
                             mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-                            tma_load_2d(pd, &map_p, &ctl->full[stage], kb * 128, py);
-                            tma_load_2d(qd, &map_q, &ctl->full[stage], kb * 128, qy);
+                            tma_load_2d(pd, &k.map_p(it.which), &ctl->full[stage], kb * 128, py);
+                            tma_load_2d(qd, &k.map_q(it.which), &ctl->full[stage], kb * 128, qy);
                         }
                         ctl->issued[pid] = n + 1;
                     }
@@ -600,7 +626,8 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         // Its time from one stage to the next is what bounds the product (every
         // instruction here counts once per stage): one wait, no other shared-memory
         // access, the descriptors by addition.
-        const uint32_t idesc0 = ((uint32_t)p.fmt_p << 7) | ((uint32_t)p.fmt_q << 10) | (1u << 23) | ((kPair ? 16u : 8u) << 24);
+        const uint32_t idesc0 = (kTwo ? 0u : ((uint32_t)p0.fmt_p << 7) | ((uint32_t)p0.fmt_q << 10)) | (1u << 23) |
+                                ((kPair ? 16u : 8u) << 24);
         const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSw128);
         const uint64_t bd0 = smem_desc(smem_u32(smem + kAStageBytes), 16, 1024, kLayoutSw128);
         // The whole warp walks the loop (the descriptors stay in uniform registers),
@@ -610,16 +637,17 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
-            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             if (it.kb1 > it.kb0) {
                 const int buf = acc & 1;
-                lin_wait<kPair>(p, ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
-                if (C::kOverlap && acc) lin_wait<kPair>(p, ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
+                lin_wait<kPair>(k.p(0), ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
+                if (C::kOverlap && acc) lin_wait<kPair>(k.p(0), ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * C::kAccStep);
-                const uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
+                uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
+                if (kTwo) idesc1 |= ((uint32_t)k.p(it.which).fmt_p << 7) | ((uint32_t)k.p(it.which).fmt_q << 10);
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
-                    if (!lin_wait<kPair>(p, ctl, &ctl->full[stage], ph, kRoleMma)) break;
+                    if (!lin_wait<kPair>(k.p(0), ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (C::kStageBytes >> 4));
@@ -672,13 +700,13 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         int n = 0, stage = 0, slot = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
-            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                lin_wait(p, ctl, &ctl->sf_full[stage], ph, kRoleScale);
+                lin_wait(k.p(0), ctl, &ctl->sf_full[stage], ph, kRoleScale);
                 if (kPair && n >= C::kSfSlots) {   // (fewer slots than stages: the slot's last MMAs are done)
                     const int u = n - C::kSfSlots;
-                    lin_wait<kPair>(p, ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale);
+                    lin_wait<kPair>(k.p(0), ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale);
                 }
                 __syncwarp();
                 tc_fence_after();
@@ -727,17 +755,18 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
         const int quarter = warp & 3, part = (warp - 8) >> 2;
         // shared tiles: the others' parts of this CTA's columns, [splits - 1][TQ / splits][128] fp32
         const float* parts_in = reinterpret_cast<const float*>(smem + C::oPart);
-        const int own = split ? TQ / p.splits : TQ;
+        const int own = split ? TQ / k.p(0).splits : TQ;
         int acc = 0;
         for (int tile = first; tile < total; tile += stride) {
-            const LinItem it = lin_item<TQ>(p, ctl, tile, rank);
+            const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const bool live = it.kb1 > it.kb0;
             const int buf = acc & 1;
             const int f = it.p0 + quarter * 32 + lane;
+            const LinParams& p = k.p(it.which);
             const bool in_p = it.p0 + quarter * 32 < p.p_rows;   // (P rows come in blocks of 32: uniform over the warp)
             const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kAccStep + part * C::kColsPerWarp);
             if (live) {
-                lin_wait<kPair>(p, ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
+                lin_wait<kPair>(k.p(0), ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
                 __syncwarp();
                 tc_fence_after();
             }
@@ -883,7 +912,7 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
             const int s = i % stages, n = last - ((last - s) % stages + stages) % stages;   // stage s's last use
             if (n < 0 || (i < stages && kPair && rank != 0)) continue;
             while (!lin_try<kPair>(i < stages ? &ctl->full[s] : &ctl->sf_full[s], (n / stages) & 1))
-                if (globaltimer() - t0 > (uint64_t)p.timeout_ns) break;
+                if (globaltimer() - t0 > (uint64_t)k.p(0).timeout_ns) break;
         }
     }
     __syncthreads();
@@ -898,24 +927,39 @@ __global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
 }
 
 template <int TQ>
-cudaError_t launch_tq(const LinParams& p, const CUtensorMap& map_p, const CUtensorMap& map_q, const CUtensorMap& map_q32, int ctas,
-                      cudaStream_t stream) {
+__global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
+    linear_kernel(const __grid_constant__ LinParams p, const __grid_constant__ CUtensorMap map_p,
+                  const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q32) {
+    linear_body<TQ>(LinOne{p, map_p, map_q, map_q32});
+}
+template <int TQ>
+__global__ void __launch_bounds__(LinCfg<TQ>::kThreads, LinCfg<TQ>::kCtasPerSm)
+    linear2_kernel(const __grid_constant__ LinPack k) {
+    linear_body<TQ>(LinTwo{k});
+}
+
+template <int TQ>
+cudaError_t launch_n(const LinPack& k, int ctas, cudaStream_t stream) {
     using C = LinCfg<TQ>;
-    static unsigned long long allowed = 0;
-    if (cudaError_t e = allow_smem(linear_kernel<TQ>, C::ctl_bytes(), allowed)) return e;
-    return launch(linear_kernel<TQ>, dim3((unsigned)ctas), C::kThreads, C::ctl_bytes(), C::kPair ? 2 : p.splits, stream, p, map_p,
-                  map_q, map_q32);
+    static unsigned long long allowed[2] = {};
+    const int cluster = C::kPair ? 2 : k.p[0].splits;
+    if (k.n > 1) {
+        if (cudaError_t e = allow_smem(linear2_kernel<TQ>, C::ctl_bytes(), allowed[1])) return e;
+        return launch(linear2_kernel<TQ>, dim3((unsigned)ctas), C::kThreads, C::ctl_bytes(), cluster, stream, k);
+    }
+    if (cudaError_t e = allow_smem(linear_kernel<TQ>, C::ctl_bytes(), allowed[0])) return e;
+    return launch(linear_kernel<TQ>, dim3((unsigned)ctas), C::kThreads, C::ctl_bytes(), cluster, stream, k.p[0], k.maps[0].p,
+                  k.maps[0].q, k.maps[0].q32);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q,
-                          const CUtensorMap& map_q32, int ctas, cudaStream_t stream) {
+cudaError_t launch_linear(const LinPack& k, int tile_q, int ctas, cudaStream_t stream) {
     switch (tile_q) {
-        case 32: return launch_tq<32>(p, map_p, map_q, map_q32, ctas, stream);
-        case 64: return launch_tq<64>(p, map_p, map_q, map_q32, ctas, stream);
-        case 128: return launch_tq<128>(p, map_p, map_q, map_q32, ctas, stream);
-        default: return launch_tq<256>(p, map_p, map_q, map_q32, ctas, stream);
+        case 32: return launch_n<32>(k, ctas, stream);
+        case 64: return launch_n<64>(k, ctas, stream);
+        case 128: return launch_n<128>(k, ctas, stream);
+        default: return launch_n<256>(k, ctas, stream);
     }
 }
 

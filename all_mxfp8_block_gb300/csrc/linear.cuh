@@ -45,12 +45,21 @@ struct LinParams {
 
 constexpr int kRoleScale = 7;
 
+// A launch's products: one, or the two of a gradient (rows first, by contraction
+// second), which then share the CTAs without a seam between them.  They agree in
+// splits and segments.
+struct LinMaps {
+    CUtensorMap p, q, q32;   // P boxes of 128 rows; Q boxes of linear_q_box(tile_q) rows, of 32 rows (tile_q 256)
+};
+struct LinPack {
+    LinMaps maps[2];
+    LinParams p[2];
+    int n;
+};
+
 // tile_q: 32, 64, 128, or 256 (the CTA-pair kernel: 256 P rows to a tile, ctas
-// in pairs, no splits).  map_q: boxes of linear_q_box(tile_q) rows; map_q32
-// (tile_q 256 only): boxes of 32 rows.  ctas: CTAs to launch, a multiple of
-// splits (of 2 for pairs)
-cudaError_t launch_linear(const LinParams& p, int tile_q, const CUtensorMap& map_p, const CUtensorMap& map_q,
-                          const CUtensorMap& map_q32, int ctas, cudaStream_t stream);
+// in pairs, no splits).  ctas: CTAs to launch, a multiple of splits (of 2 for pairs)
+cudaError_t launch_linear(const LinPack& k, int tile_q, int ctas, cudaStream_t stream);
 inline int linear_q_box(int tile_q) { return tile_q == 256 ? 128 : tile_q; }
 inline int linear_p_tile(int tile_q) { return tile_q == 256 ? 256 : 128; }
 // CTAs of the kernel that one SM holds at once
