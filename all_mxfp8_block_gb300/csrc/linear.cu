@@ -135,23 +135,24 @@ __device__ __forceinline__ void lin_report(const LinParams& p, int role, long lo
     __threadfence();
 }
 
-// Bounded wait for an mbarrier phase.  After a time-out anywhere in the CTA
-// every later wait returns at once, so that all roles reach the end together.
 // kCluster: the phase is completed by arrivals from the other CTA of a pair.
 template <bool kCluster = false>
 __device__ __forceinline__ bool lin_try(uint64_t* bar, uint32_t parity) {
     return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
 }
-// False once the CTA gave up.
+// Bounded wait of a whole warp for an mbarrier phase, with one answer for all its
+// lanes; false once the CTA gave up.  After a time-out every later wait that would
+// block returns at once and no role starts another tile, so that all reach the
+// end together.
 template <bool kCluster = false>
 __device__ __forceinline__ bool lin_wait(const LinParams& p, LinCtl* ctl, uint64_t* bar, uint32_t parity, int role) {
-    if (lin_try<kCluster>(bar, parity)) return true;
+    if (__all_sync(kLanes, lin_try<kCluster>(bar, parity))) return true;
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1;; ++n) {
-        if (lin_try<kCluster>(bar, parity)) return true;
-        if (ctl->abort) return false;
-        if ((n & 63) == 0 && globaltimer() - t0 > (uint64_t)p.timeout_ns) {
-            lin_report(p, role, (long long)parity);
+        if (__all_sync(kLanes, lin_try<kCluster>(bar, parity))) return true;
+        if (__any_sync(kLanes, ctl->abort)) return false;
+        if ((n & 63) == 0 && __any_sync(kLanes, globaltimer() - t0 > (uint64_t)p.timeout_ns)) {
+            if (threadIdx.x % 32 == 0) lin_report(p, role, (long long)parity);
             ctl->abort = 1;
             return false;
         }
@@ -571,6 +572,10 @@ __device__ __forceinline__ void linear_body(const K& k) {
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
         const uint64_t keep = l2_policy_evict_last();
         for (int tile = first; tile < total; tile += stride) {
+            if (__any_sync(kLanes, ctl->abort)) {
+                if (split) lin_tile_end(tile + stride < total);
+                continue;
+            }
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const LinParams& p = k.p(it.which);
             const int qa = it.q0 >> 7;                                          // first scale tile of the Q rows
@@ -637,6 +642,10 @@ __device__ __forceinline__ void linear_body(const K& k) {
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
+            if (__any_sync(kLanes, ctl->abort)) {
+                if (split) lin_tile_end(tile + stride < total);
+                continue;
+            }
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             if (it.kb1 > it.kb0) {
                 const int buf = acc & 1;
@@ -700,15 +709,18 @@ __device__ __forceinline__ void linear_body(const K& k) {
         int n = 0, stage = 0, slot = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
+            if (__any_sync(kLanes, ctl->abort)) {
+                if (split) lin_tile_end(tile + stride < total);
+                continue;
+            }
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
             for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-                lin_wait(k.p(0), ctl, &ctl->sf_full[stage], ph, kRoleScale);
+                if (!lin_wait(k.p(0), ctl, &ctl->sf_full[stage], ph, kRoleScale)) break;
                 if (kPair && n >= C::kSfSlots) {   // (fewer slots than stages: the slot's last MMAs are done)
                     const int u = n - C::kSfSlots;
-                    lin_wait<kPair>(k.p(0), ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale);
+                    if (!lin_wait<kPair>(k.p(0), ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale)) break;
                 }
-                __syncwarp();
                 tc_fence_after();
                 const uint32_t t =
                     tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
@@ -767,7 +779,6 @@ __device__ __forceinline__ void linear_body(const K& k) {
             const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kAccStep + part * C::kColsPerWarp);
             if (live) {
                 lin_wait<kPair>(k.p(0), ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
-                __syncwarp();
                 tc_fence_after();
             }
             if (p.by_contraction && it.b1 <= it.b0) {   // a group without tokens
@@ -903,16 +914,18 @@ __device__ __forceinline__ void linear_body(const K& k) {
     }
     __syncthreads();
     if (ctl->abort && threadIdx.x == 0) {
-        // loads may still be in flight into this CTA's shared memory: give them
-        // time to land (bounded) before the CTA ends (pair: the even CTA's
-        // barrier counts both CTAs' loads, and both end together below)
+        // loads and MMAs may still be in flight on this CTA's memory: they end
+        // within microseconds (pair: the even CTA's barrier counts both CTAs'
+        // loads, and both end together below); 1 ms at least, 10 at most
         const uint64_t t0 = globaltimer();
         const int last = max(max(ctl->issued[0], ctl->issued[1]), ctl->issued[2]) - 1;
         for (int i = 0; i < 2 * stages; ++i) {   // operands, then scale tiles
             const int s = i % stages, n = last - ((last - s) % stages + stages) % stages;   // stage s's last use
             if (n < 0 || (i < stages && kPair && rank != 0)) continue;
             while (!lin_try<kPair>(i < stages ? &ctl->full[s] : &ctl->sf_full[s], (n / stages) & 1))
-                if (globaltimer() - t0 > (uint64_t)k.p(0).timeout_ns) break;
+                if (globaltimer() - t0 > 10000000) break;
+        }
+        while (globaltimer() - t0 < 1000000) {
         }
     }
     __syncthreads();

@@ -561,7 +561,8 @@ int mxa2a_linear_set_option(mxa2a_linear* l, int key, int64_t v) {
     if (!l) return MXA2A_ERR_NULL_PTR;
     switch (key) {
         case MXA2A_OPT_TIMEOUT_NS:
-            if (v < 1000) return MXA2A_ERR_INVALID_OPTION;
+            // (its waits are for this GPU's own work, microseconds: only a stall is to run out)
+            if (v < 1000000) return MXA2A_ERR_INVALID_OPTION;
             l->timeout_ns = v;
             return MXA2A_OK;
         case MXA2A_OPT_ELEM_TYPES:

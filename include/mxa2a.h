@@ -687,8 +687,8 @@ int mxa2a_linear_backward(mxa2a_linear *layer, int64_t rows, const void *dy, con
  * producer, 3 MMA issuer, 4 epilogue, 7 scale copy). */
 int mxa2a_linear_get_status(mxa2a_linear *layer, mxa2a_status *out);
 
-/* MXA2A_OPT_TIMEOUT_NS and MXA2A_OPT_ELEM_TYPES (A is x, B is w), and, for get
- * only, MXA2A_INFO_LAUNCHES and MXA2A_INFO_WORKSPACE_BYTES. */
+/* MXA2A_OPT_TIMEOUT_NS (at least 1e6) and MXA2A_OPT_ELEM_TYPES (A is x, B is w), and, for
+ * get only, MXA2A_INFO_LAUNCHES and MXA2A_INFO_WORKSPACE_BYTES. */
 int mxa2a_linear_set_option(mxa2a_linear *layer, int key, int64_t value);
 int mxa2a_linear_get_option(mxa2a_linear *layer, int key, int64_t *value);
 

@@ -378,6 +378,60 @@ def test_backward_without_rows():
     assert (dw == 0).all() and (db == 0).all()
 
 
+def test_backward_one_layer_many_shapes():
+    # one plan and its workspace, the rows varying from call to call, on another stream; one and two products to a launch
+    l = mxa2a.Linear(3, 1200, 288, 160, training=True)
+    s = torch.cuda.Stream()
+    for lens in ([400, 0, 700], [1, 0, 0], [33, 64, 5], [400, 0, 700]):
+        i = layer_inputs(lens, 288, 160, sum(lens))
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            check_backward(i, "silu", "e4m3", layer=l)
+            check_backward(i, "none", "e5m2", want=("dw", "dbias"), layer=l)
+
+
+def test_backward_repeats_bitwise_and_graph():
+    i = layer_inputs([70, 0, 200], 288, 416, 3)
+    rows, N, K = i["rows"], 288, 416
+    rng = np.random.default_rng(0)
+    dy, z = (torch.from_numpy(rng.standard_normal((rows, N))).bfloat16().cuda() for _ in range(2))
+    xt = np.zeros((K, R.up(rows, 32)))
+    xt[:, :rows] = i["x"].T
+    XT, WT = R.mx(xt), R.mx(i["w"].transpose(0, 2, 1).copy())
+    l = mxa2a.Linear(3, rows, N, K, training=True)
+    dx, dw = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, N, K, device="cuda")
+    db = torch.zeros(3, N, device="cuda")
+
+    def run():
+        l.backward(rows, dy, z, ACT["gelu"], TYPE["e4m3"], XT[0], XT[1], WT[0], WT[1], dx, dw, TYPE["f32"], db, i["off"], i["cnt"])
+
+    run()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in (dx, dw, db)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(3):
+        for t in (dx, dw, db):
+            t.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        used = int(i["starts"][-1])
+        assert torch.equal(first[0][:used], dx[:used]) and torch.equal(first[1], dw) and torch.equal(first[2], db)
+    assert l.status()["code"] == 0
+
+
+def test_layer_options():
+    l = mxa2a.Linear(1, 32, 32, 32)
+    assert l.get_option(mxa2a.MXA2A_OPT_TIMEOUT_NS) == 2_000_000_000
+    l.set_option(mxa2a.MXA2A_OPT_TIMEOUT_NS, 1_000_000)
+    assert l.get_option(mxa2a.MXA2A_OPT_TIMEOUT_NS) == 1_000_000
+    for key, bad in ((mxa2a.MXA2A_OPT_TIMEOUT_NS, 999_999), (mxa2a.MXA2A_OPT_ELEM_TYPES, 4), (mxa2a.MXA2A_OPT_ELEM_TYPES, -1),
+                     (mxa2a.MXA2A_OPT_SPLIT_K, 1)):
+        with pytest.raises(mxa2a.Mxa2aError):
+            l.set_option(key, bad)
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
 def test_activation_slope_against_differences(act):
     # one token: dbias is dy * act'(z), and act' is the difference quotient of the 64-bit activation
