@@ -86,8 +86,6 @@ struct LinCfg {
     static constexpr int kQCols = TQ / 32 < 4 ? 4 : TQ / 32;                        // TMEM columns of its scales
     static constexpr uint32_t kSfCol = kAccStep + TQ;
     static constexpr uint32_t kSfCols = 4 + kQCols;
-    // stages whose scales are in tensor memory (the pair kernel has columns left for 5 of its 6)
-    static constexpr int kSfSlots = kPair ? 5 : kStages;
     static constexpr uint32_t kTmem = TQ <= 32 ? 128 : (TQ == 64 ? 256 : 512);
     static constexpr int kQRows = kPair ? 128 : TQ;                                 // Q rows this CTA holds of a tile
     static constexpr int kQBytes = kQRows * 128;
@@ -99,7 +97,7 @@ struct LinCfg {
     static constexpr size_t oSfq = oSfp + (size_t)kStages * 512;
     static constexpr size_t oCtl = oSfq + (size_t)kStages * kQAtoms * 512;
     static constexpr size_t ctl_bytes();
-    static_assert(kSfCol + kSfSlots * kSfCols <= kTmem, "tensor memory columns");
+    static_assert(kSfCol + kStages * kSfCols <= kTmem, "tensor memory columns");
 };
 
 struct __align__(8) LinCtl {
@@ -638,7 +636,7 @@ __device__ __forceinline__ void linear_body(const K& k) {
         // The whole warp walks the loop (the descriptors stay in uniform registers),
         // one elected lane issues.
         const bool leader = elect_one();
-        int stage = 0, slot = 0, acc = 0;
+        int stage = 0, acc = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (kPair && rank != 0) break;
@@ -658,7 +656,7 @@ __device__ __forceinline__ void linear_body(const K& k) {
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!lin_wait<kPair>(k.p(0), ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
-                    const uint32_t sf = tmem + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
+                    const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (C::kStageBytes >> 4));
                     const int k0 = max(0, it.b0 - kb * 4), k1 = min(4, it.b1 - kb * 4);
@@ -689,7 +687,6 @@ __device__ __forceinline__ void linear_body(const K& k) {
                         stage = 0;
                         ph ^= 1;
                     }
-                    if (kPair && ++slot == C::kSfSlots) slot = 0;
                 }
                 if (leader) {
                     if constexpr (kPair)
@@ -706,7 +703,7 @@ __device__ __forceinline__ void linear_body(const K& k) {
         // ---------------------------------------------------------- scale warps
         const int quarter = warp & 3;
         const uint32_t full0 = kPair ? mapa_shared(smem_u32(&ctl->full[0]), 0) : 0u;
-        int n = 0, stage = 0, slot = 0;
+        int stage = 0;
         uint32_t ph = 0;
         for (int tile = first; tile < total; tile += stride) {
             if (__any_sync(kLanes, ctl->abort)) {
@@ -715,15 +712,12 @@ __device__ __forceinline__ void linear_body(const K& k) {
             }
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const int shift = (it.q0 & 127) >> 5;   // 32-row groups before the tile in its first scale tile
-            for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+            for (int kb = it.kb0; kb < it.kb1; ++kb) {
                 if (!lin_wait(k.p(0), ctl, &ctl->sf_full[stage], ph, kRoleScale)) break;
-                if (kPair && n >= C::kSfSlots) {   // (fewer slots than stages: the slot's last MMAs are done)
-                    const int u = n - C::kSfSlots;
-                    if (!lin_wait<kPair>(k.p(0), ctl, &ctl->empty[u % C::kStages], (u / C::kStages) & 1, kRoleScale)) break;
-                }
                 tc_fence_after();
-                const uint32_t t =
-                    tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)(kPair ? slot : stage) * C::kSfCols;
+                // (as many places as stages: the producer filled this stage after the
+                // last MMAs that read its place; a wait of its own for them cost 6 %)
+                const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + C::kSfCol + (uint32_t)stage * C::kSfCols;
                 tmem_st_32x32b_x4(t, reinterpret_cast<const uint4*>(smem + C::oSfp + stage * 512)[lane]);
                 const uint8_t* sq = smem + C::oSfq + (size_t)stage * C::kQAtoms * 512;
                 // words 4 a + shift .. of the tiles' concatenated columns
@@ -755,7 +749,6 @@ __device__ __forceinline__ void linear_body(const K& k) {
                     stage = 0;
                     ph ^= 1;
                 }
-                if (kPair && ++slot == C::kSfSlots) slot = 0;
             }
             __syncwarp();
             if (split) lin_tile_end(tile + stride < total);
