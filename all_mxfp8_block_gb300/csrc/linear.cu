@@ -25,6 +25,14 @@
 // contraction range may start and end inside a 128-wide block: the MMA's
 // 32-wide steps outside it are not issued.
 //
+// What bounds it: a few tokens, the weights' bytes and the launch's latency (1
+// token x 7168 x 8192: 15.5 us, 3.9 TB/s; 8 tokens x 4 of 16 experts x 2048 x
+// 7168: 36 us, 6.1 TB/s); wide tiles, the MMAs with the time of a stage around
+// the ring close behind, and over longer runs the power limit (8192^3: 290 us,
+// 3.79 PFLOP/s; the MMAs alone 256 us).  With an expert's weights read for 512
+// rows the loads come from HBM and are the slower side (32 experts x 512 x 2048
+// x 7168: 154 us, 130 us with one weight matrix).
+//
 // Every wait is bounded; after one ran out the CTA goes on without waiting (its
 // output is then undefined) and the status block tells.
 #include <algorithm>
@@ -174,6 +182,14 @@ __device__ __forceinline__ int seg_start(const LinParams& p, int g, int limit) {
     return max(0, min(*(p.offsets + g), limit)) & ~31;
 }
 
+// Q tiles of a group of Q rows
+template <int TQ>
+__device__ __forceinline__ int q_tiles(const LinParams& p, int g) {
+    int len = p.q_rows;
+    if (p.offsets) len = max(0, min(*(p.offsets + g + 1), p.q_rows) - seg_start(p, g, p.q_rows));
+    return (len + TQ - 1) / TQ;
+}
+
 // a launch's one product, or its two
 struct LinOne {
     static constexpr bool kTwo = false;
@@ -199,16 +215,16 @@ __device__ __forceinline__ LinItem lin_item(const K& k, const LinCtl* ctl, int t
     it.which = K::kTwo && tile >= ctl->rows_total ? 1 : 0;
     if (it.which) tile -= ctl->rows_total;
     const LinParams& p = k.p(it.which);
-    int p_tile, q_tile, qt;
+    // (Every role works this out for every tile: three divisions less are half a
+    // percent of 16384 x 4096 x 4096.)
+    int r, qt;   // tile inside the group; the group's Q tiles
     if (p.by_contraction) {
         const int per = p.pt * p.qt;
         it.group = tile / per;
-        const int r = tile - it.group * per;
-        q_tile = r / p.pt;
-        p_tile = r - q_tile * p.pt;
+        r = tile - it.group * per;
+        qt = p.qt;
         it.q0 = 0;
         it.q_end = it.q_live = p.q_rows;
-        qt = p.qt;
         it.b0 = 0;
         it.b1 = p.blocks;
         if (p.offsets) {
@@ -222,30 +238,31 @@ __device__ __forceinline__ LinItem lin_item(const K& k, const LinCtl* ctl, int t
             if (ctl->start[mid] <= tile) lo = mid; else hi = mid - 1;
         }
         it.group = lo;
-        const int first = ctl->start[lo];
-        qt = (ctl->start[lo + 1] - first) / p.pt;
-        const int r = tile - first;
-        // bands of 2048 P rows, all Q tiles of a band before the next: the CTAs
-        // in flight share P and Q tiles in L2
-        constexpr int kBand = LinCfg<TQ>::kPair ? 8 : 16;
-        const int band = r / (kBand * qt), np = min(kBand, p.pt - band * kBand), rb = r - band * kBand * qt;
-        q_tile = rb / np;
-        p_tile = band * kBand + rb - q_tile * np;
-        int o = 0;
+        r = tile - ctl->start[lo];
+        it.q0 = 0;
         it.q_end = it.q_live = p.q_rows;
+        qt = q_tiles<TQ>(p, lo);
         if (p.offsets) {
-            o = seg_start(p, lo, p.q_rows);
+            it.q0 = seg_start(p, lo, p.q_rows);
             it.q_end = lo + 1 == p.groups ? min(*(p.offsets + lo + 1), p.q_rows) : seg_start(p, lo + 1, p.q_rows);
-            it.q_live = o + min(max(0, it.q_end - o), max(0, *(p.counts + lo)));
+            it.q_live = it.q0 + min(max(0, it.q_end - it.q0), max(0, *(p.counts + lo)));
         }
-        it.q0 = o;
         it.b0 = 0;
         it.b1 = p.blocks;
     }
+    // bands of 2048 P rows, all Q tiles of a band before the next: the CTAs in
+    // flight share P and Q tiles in L2
+    constexpr int kBand = LinCfg<TQ>::kPair ? 8 : 16;
+    const int band = p.pt <= kBand ? 0 : r / (kBand * qt), np = min(kBand, p.pt - band * kBand), rb = r - band * kBand * qt;
+    const int q_tile = np == kBand ? rb / kBand : rb / np;
+    const int p_tile = band * kBand + rb - q_tile * np;
     // the segment's tiles are equally wide, in 32-row steps (none is empty: the
     // width is at most TQ): no narrow last tile that costs a stage's latency for
     // little work
-    const int width = ((it.q_end - it.q0 + qt - 1) / qt + 31) & ~31;
+    const int steps = (it.q_end - it.q0 + 31) >> 5;
+    int width = 32;
+#pragma unroll
+    for (int i = 1; i < TQ / 32; ++i) width += steps > i * qt ? 32 : 0;
     it.q0 += q_tile * width;
     it.q_end = min(it.q_end, it.q0 + width);
     it.p0 = p_tile * (LinCfg<TQ>::kPair ? 256 : 128) + (LinCfg<TQ>::kPair ? rank * 128 : 0);
@@ -522,15 +539,7 @@ __device__ __forceinline__ void linear_body(const K& k) {
             for (int g0 = 0; g0 < p0.groups; g0 += 32) {
                 const int g = g0 + lane;
                 int n = 0;
-                if (g < p0.groups) {
-                    int len = p0.q_rows;
-                    if (p0.offsets) {
-                        const int lo = seg_start(p0, g, p0.q_rows);
-                        const int hi = min(*(p0.offsets + g + 1), p0.q_rows);
-                        len = max(0, hi - lo);
-                    }
-                    n = (len + TQ - 1) / TQ * p0.pt;
-                }
+                if (g < p0.groups) n = q_tiles<TQ>(p0, g) * p0.pt;
                 int inc = n;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
