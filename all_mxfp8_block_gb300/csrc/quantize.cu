@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[p][j] = act_back2<kAct>(v[p][j], make_float2(z[2 * j], z[2 * j + 1]));
         }
-        if (!live[p]) {
+        // (the vote: no selects on whole tiles; the silu pass without codes 60.2 -> 56.5 us on 16384 x 4096)
+        if (__any_sync(kLanes, !live[p]) && !live[p]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[p][j] = make_float2(0.f, 0.f);
         }
@@ -114,13 +115,11 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     if (!q.codes_t && !q.colsum) return;
 #pragma unroll
     for (int p = 0; p < kPass; ++p) {
-        // (the upper four threads of a row swap the order of their halves: no bank conflicts)
+        // (the columns of the upper half of the tile lie in pairs of 4 swapped: no bank conflicts)
         float4* t = tile + (ty + p * 32) * (kTileCols / 4) + tx * 2;
-        const float4 lo = make_float4(v[p][0].x, v[p][0].y, v[p][1].x, v[p][1].y);
-        const float4 hi = make_float4(v[p][2].x, v[p][2].y, v[p][3].x, v[p][3].y);
         const int swap = tx >> 2;
-        t[swap] = swap ? hi : lo;
-        t[swap ^ 1] = swap ? lo : hi;
+        t[swap] = make_float4(v[p][0].x, v[p][0].y, v[p][1].x, v[p][1].y);
+        t[swap ^ 1] = make_float4(v[p][2].x, v[p][2].y, v[p][3].x, v[p][3].y);
     }
     __syncthreads();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -131,7 +130,7 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     float2 s01 = make_float2(0.f, 0.f), s23 = s01;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        u[i] = tile[(rb * 32 + rg * 8 + i) * (kTileCols / 4) + c4];
+        u[i] = tile[(rb * 32 + rg * 8 + i) * (kTileCols / 4) + (c4 ^ (c4 >> 3))];
         s01 = add2(s01, make_float2(u[i].x, u[i].y));
         s23 = add2(s23, make_float2(u[i].z, u[i].w));
     }
@@ -151,22 +150,33 @@ __global__ void __launch_bounds__(kQThreads, 4) quantize_kernel(Quantize q, int 
     // (a thread's 4 columns are neighbours in one 32-row group of their scale tile)
     uint8_t* scale_t = q.scale_t + ((size_t)g * row_tiles + row_tile) * ct * 512;
     uint8_t* word = scale_t + (size_t)(c >> 7) * 512 + (c & 31) * 16 + ((c & 127) >> 5) * 4 + rb;
+    float inv[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float w[8], m = 0.f;
+        float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = j == 0 ? u[i].x : j == 1 ? u[i].y : j == 2 ? u[i].z : u[i].w;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) m = abs_max(m, w[i], w[i + 1]);
+        for (int i = 0; i < 8; i += 2) m = abs_max(m, (&u[i].x)[j], (&u[i + 1].x)[j]);
         m = max_nan(m, __shfl_xor_sync(kLanes, m, 8));
         m = max_nan(m, __shfl_xor_sync(kLanes, m, 16));
         const uint32_t byte = mx_scale_byte(__float_as_uint(m), emax);
-        const float inv = mx_inv_scale(byte);
-        if (in_t)
-            *reinterpret_cast<uint2*>(codes_t + j * ld_t) =
-                make_uint2(mx_codes4<kE5m2>(make_float2(w[0], w[1]), make_float2(w[2], w[3]), inv),
-                           mx_codes4<kE5m2>(make_float2(w[4], w[5]), make_float2(w[6], w[7]), inv));
+        inv[j] = mx_inv_scale(byte);
         if (in_c && rg == 0) word[j * 16] = in_t ? (uint8_t)byte : 0;
+    }
+    // (two columns a multiplication: they are neighbours in registers, the rows are not)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 lo = mul2(make_float2(u[i].x, u[i].y), make_float2(inv[0], inv[1]));
+        const float2 hi = mul2(make_float2(u[i].z, u[i].w), make_float2(inv[2], inv[3]));
+        u[i] = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    if (in_t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = fp8x2<kE5m2>((&u[2 * i].x)[j], (&u[2 * i + 1].x)[j]);
+            *reinterpret_cast<uint2*>(codes_t + j * ld_t) = make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+        }
     }
     // the words of the last scale tile past the last column
     if (c0 + kTileCols >= cols)
