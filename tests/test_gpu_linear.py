@@ -421,6 +421,22 @@ def test_backward_repeats_bitwise_and_graph():
     assert l.status()["code"] == 0
 
 
+def test_backward_bad_segments_stay_inside():
+    # as test_linear_bad_segments_stay_inside, for the three gradients
+    i = layer_inputs([64, 64], 64, 128, 1)
+    rows, N, K = i["rows"], 64, 128
+    XT, WT = R.mx(i["x"].T.copy()), R.mx(i["w"].transpose(0, 2, 1).copy())
+    dy = torch.ones(rows, N, dtype=torch.bfloat16, device="cuda")
+    l = mxa2a.Linear(2, rows, N, K, training=True)
+    for off, cnt in (([0, 70, 4000], [64, 64]), ([-40, 64, 128], [1 << 30, -3]), ([0, 128, 64], [64, 64]), ([5, 3, 1], [1, 1])):
+        dx = torch.full((rows + 64, K), 7.0, dtype=torch.bfloat16, device="cuda")
+        dw, db = torch.full((3, N, K), 7.0, device="cuda"), torch.full((3, N), 7.0, device="cuda")
+        l.backward(rows, dy, None, 0, TYPE["e4m3"], XT[0], XT[1], WT[0], WT[1], dx, dw, TYPE["f32"], db,
+                   torch.tensor(off, dtype=torch.int32).cuda(), torch.tensor(cnt, dtype=torch.int32).cuda())
+        torch.cuda.synchronize()
+        assert (dx[rows:] == 7.0).all() and (dw[2] == 7.0).all() and (db[2] == 7.0).all() and l.status()["code"] == 0
+
+
 def test_layer_options():
     l = mxa2a.Linear(1, 32, 32, 32)
     assert l.get_option(mxa2a.MXA2A_OPT_TIMEOUT_NS) == 2_000_000_000
