@@ -33,8 +33,8 @@
 // rows the loads come from HBM and are the slower side (32 experts x 512 x 2048
 // x 7168: 154 us, 130 us with one weight matrix).
 //
-// Every wait is bounded; after one ran out the CTA goes on without waiting (its
-// output is then undefined) and the status block tells.
+// Every wait is bounded; after one ran out no role of the CTA starts another tile
+// (the output is then undefined) and the status block tells.
 #include <algorithm>
 
 #include "launch.cuh"

@@ -306,12 +306,12 @@ int layer_device(const mxa2a_linear* l) {
 //   last row are multiplied for nothing, and a wider tile re-reads the P rows
 //   less often.
 // * Rows for 256-wide tiles go to the CTA-pair kernel once its tiles fill half
-//   of the pairs (1024 x 4096 x 4096, 64 tiles: 19.8 us against 21.9 us on single
-//   CTAs; 512 x 4096 x 4096, 32 tiles: 18.1 against 13.9), else to single CTAs on
+//   of the pairs (1024 x 4096 x 4096, 64 tiles: 18.6 us against 22.5 us on single
+//   CTAs; 512 x 4096 x 4096, 32 tiles: 17.0 against 14.4), else to single CTAs on
 //   128-wide tiles.
 // * A launch with fewer tiles than CTAs splits the contraction over a cluster,
 //   as far as every part keeps two 128-wide blocks (1 token x 7168 x 8192, 56
-//   tiles: 20.3, 17.0, 23.0 us for 2, 4, 8 parts; 8 parts no longer fit at once).
+//   tiles: 18.6, 15.6, 20.9 us for 2, 4, 8 parts; 8 parts no longer fit at once).
 struct Shape {
     int tq, splits, ctas;
 };
@@ -519,10 +519,10 @@ int mxa2a_linear_backward(mxa2a_linear* l, int64_t rows, const void* dy, const v
     }
     if (n == 2) {
         // Both products in one launch where they want tiles of one width: no seam
-        // between them (300 x 1056 x 1024: 20.8 -> 13.7 us).  On pairs only up to 8
-        // tiles each: choosing the product per tile costs that kernel 3 % (16380 x
-        // 320 x 1120 over 10 experts, 6 tiles each: 58.8 -> 51.3 us; 16384 x 4096 x
-        // 4096 over 8, 41 each: 491 -> 504 us).
+        // between them (300 x 1056 x 1024: 20.9 -> 13.8 us).  On pairs only up to 8
+        // tiles each: choosing the product per tile costs that kernel 1 to 3 %, which
+        // outweighs the seam with many (16380 x 320 x 1120 over 10 experts, 6 tiles
+        // each: 57.6 -> 49.7 us; 16384 x 4096 x 4096 over 8, 41 each: 503 -> 507 us).
         auto shape = [&](int i) { return choose_shape(l->sms, d[i].tile_rows, product_blocks(d[i]), [&](int tq) { return product_tiles(d[i], tq); }); };
         const Shape a = shape(0), b = shape(1);
         if (a.tq == b.tq) {
