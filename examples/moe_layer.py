@@ -37,11 +37,18 @@ def bf16(*shape):
     return torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")
 
 
+def check(name, t, dtype, *shape):
+    """The library takes addresses: what a call reads or writes has to be what it is taken for."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} wanted, got {t.dtype} {list(t.shape)}")
+
+
 class MoELayer:
     """Buffers and plans for up to ``tokens`` tokens a call; hidden and ffn multiples of 32."""
 
     def __init__(self, tokens, topk, experts, hidden, ffn, training=False):
-        self.k, self.E, self.H, self.F = topk, experts, hidden, ffn
+        self.tokens, self.k, self.E, self.H, self.F = tokens, topk, experts, hidden, ffn
+        self.T = None         # tokens of the forward pass that a backward pass may follow
         self.rows = rows = max(ALIGN, m.mxa2a_moe_rows(tokens, topk, experts, ALIGN))
         i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
         self.offsets, self.counts, self.pos = i32(experts + 1), i32(experts), i32(tokens * topk)
@@ -64,6 +71,10 @@ class MoELayer:
 
     def load(self, W1, W2, b1=None):
         """W1 fp32 [experts][ffn][hidden], W2 [experts][hidden][ffn], b1 [experts][ffn]: quantised once per update."""
+        check("W1", W1, torch.float32, self.E, self.F, self.H)
+        check("W2", W2, torch.float32, self.E, self.H, self.F)
+        if b1 is not None:
+            check("b1", b1, torch.float32, self.E, self.F)
         t = self.training
         m.mxa2a_quantize(W1, F32, self.H, self.E, self.F, self.H, E4M3, self.w1, self.w1_s,
                          self.w1_t if t else None, self.w1_ts if t else None)
@@ -71,14 +82,21 @@ class MoELayer:
                          self.w2_t if t else None, self.w2_ts if t else None)
         self.b1 = b1
 
-    def _sort(self, expert):
-        self.T = expert.shape[0]
-        m.mxa2a_moe_sort(self.T, self.k, self.E, ALIGN, self.rows, expert, self.offsets, self.counts, self.pos, None)
+    def _sort(self, x, expert, weight):
+        # (pos holds `tokens` tokens: the sort only checks the rows, whose padding has room for more)
+        T = expert.shape[0]
+        if T > self.tokens:
+            raise ValueError(f"{T} tokens: this layer takes up to {self.tokens}")
+        check("x", x, torch.bfloat16, T, self.H)
+        check("expert", expert, torch.int32, T, self.k)
+        check("weight", weight, torch.float32, T, self.k)
+        m.mxa2a_moe_sort(T, self.k, self.E, ALIGN, self.rows, expert, self.offsets, self.counts, self.pos, None)
+        return T
 
     def serve(self, x, expert, weight):
         """x bf16 [T][hidden], expert int32 [T][topk], weight fp32 [T][topk]; returns bf16 [T][hidden]."""
-        self._sort(expert)
-        T, out = self.T, torch.empty_like(x)
+        T, out = self._sort(x, expert, weight), torch.empty_like(x)
+        self.T = None         # (the rows of a forward pass are no longer there)
         m.mxa2a_moe_dispatch(T, self.k, self.E, self.H, self.rows, x, BF16, self.H, self.pos, self.offsets, self.counts,
                              self.x, E4M3, self.x_s)
         self.up.run(self.rows, self.x, self.x_s, self.w1, self.w1_s, self.h, E4M3, self.h_s, self.offsets, self.counts,
@@ -89,9 +107,8 @@ class MoELayer:
 
     def forward(self, x, expert, weight):
         """As serve, keeping what backward needs."""
-        self._sort(expert)
-        T, H, F, rows, out = self.T, self.H, self.F, self.rows, torch.empty_like(x)
-        self.weight = weight
+        T, H, F, rows, out = self._sort(x, expert, weight), self.H, self.F, self.rows, torch.empty_like(x)
+        self.T, self.weight = T, weight
         m.mxa2a_moe_dispatch(T, self.k, self.E, H, rows, x, BF16, H, self.pos, self.offsets, self.counts, self.xb, BF16)
         m.mxa2a_quantize(self.xb, BF16, H, 1, rows, H, E4M3, self.x, self.x_s, self.x_t, self.x_ts)
         self.up.run(rows, self.x, self.x_s, self.w1, self.w1_s, self.hb, BF16, None, self.offsets, self.counts,
@@ -103,6 +120,9 @@ class MoELayer:
 
     def backward(self, dout):
         """dout bf16 [T][hidden]: gradients of x, the routing weights, W1, W2 (fp32) and b1."""
+        if self.T is None:
+            raise ValueError("no forward pass to take the gradient of")
+        check("dout", dout, torch.bfloat16, self.T, self.H)
         T, E, H, F, rows = self.T, self.E, self.H, self.F, self.rows
         f32 = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
         dweight, dW1, dW2, db1 = f32(T, self.k), f32(E, F, H), f32(E, H, F), f32(E, F)
