@@ -33,8 +33,9 @@
 // rows the loads come from HBM and are the slower side (32 experts x 512 x 2048
 // x 7168: 154 us, 130 us with one weight matrix).
 //
-// Every wait is bounded; after one ran out no role of the CTA starts another tile
-// (the output is then undefined) and the status block tells.
+// Every wait is bounded; after one ran out no role of the CTA starts another tile,
+// a tile given up is not stored (the output is undefined then) and the status
+// block tells.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -656,13 +657,14 @@ __device__ __forceinline__ void linear_body(const K& k) {
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             if (it.kb1 > it.kb0) {
                 const int buf = acc & 1;
-                lin_wait<kPair>(k.p(0), ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
-                if (C::kOverlap && acc) lin_wait<kPair>(k.p(0), ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
+                bool ready = lin_wait<kPair>(k.p(0), ctl, &ctl->acc_empty[buf], ((acc >> 1) & 1) ^ 1, kRoleMma);
+                if (C::kOverlap && acc) ready &= lin_wait<kPair>(k.p(0), ctl, &ctl->acc_part[buf ^ 1], ((acc - 1) >> 1) & 1, kRoleMma);
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * C::kAccStep);
                 uint32_t idesc1 = idesc0 | ((uint32_t)(it.nq >> 3) << 17);
                 if (kTwo) idesc1 |= ((uint32_t)k.p(it.which).fmt_p << 7) | ((uint32_t)k.p(it.which).fmt_q << 10);
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                int kb = ready ? it.kb0 : it.kb1 + 1;   // (a tile given up ends elsewhere than at kb1)
+                for (; kb < it.kb1; ++kb) {
                     if (!lin_wait<kPair>(k.p(0), ctl, &ctl->full[stage], ph, kRoleMma)) break;
                     tc_fence_after();
                     const uint32_t sf = tmem + C::kSfCol + (uint32_t)stage * C::kSfCols;
@@ -697,7 +699,7 @@ __device__ __forceinline__ void linear_body(const K& k) {
                         ph ^= 1;
                     }
                 }
-                if (leader) {
+                if (leader && kb == it.kb1) {   // (sums of a tile given up are handed to nobody)
                     if constexpr (kPair)
                         tc_commit_pair_multicast(&ctl->acc_full[buf], 0x3);
                     else
@@ -772,6 +774,10 @@ __device__ __forceinline__ void linear_body(const K& k) {
         const int own = split ? TQ / k.p(0).splits : TQ;
         int acc = 0;
         for (int tile = first; tile < total; tile += stride) {
+            if (__any_sync(kLanes, ctl->abort)) {
+                if (split) lin_tile_end(tile + stride < total);
+                continue;
+            }
             const LinItem it = lin_item<TQ>(k, ctl, tile, rank);
             const bool live = it.kb1 > it.kb0;
             const int buf = acc & 1;
@@ -780,7 +786,10 @@ __device__ __forceinline__ void linear_body(const K& k) {
             const bool in_p = it.p0 + quarter * 32 < p.p_rows;   // (P rows come in blocks of 32: uniform over the warp)
             const uint32_t t = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * C::kAccStep + part * C::kColsPerWarp);
             if (live) {
-                lin_wait<kPair>(k.p(0), ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi);
+                if (!lin_wait<kPair>(k.p(0), ctl, &ctl->acc_full[buf], (acc >> 1) & 1, kRoleEpi)) {   // no sums: nothing is stored
+                    if (split) lin_tile_end(tile + stride < total);
+                    continue;
+                }
                 tc_fence_after();
             }
             if (p.by_contraction && it.b1 <= it.b0) {   // a group without tokens
