@@ -215,7 +215,7 @@ struct mxa2a_linear {
     int64_t timeout_ns = 2000000000LL;
     int elem_types = 0;
     int launches = 0;
-    unsigned long long launch_id = 0, checked_launch = 0;
+    unsigned long long launch_id = 0;
     // workspace: status | (training) dz codes, their scale tiles, the transpose's, the bias sums' blocks
     uint8_t* ws = nullptr;
     size_t ws_bytes = 0;
@@ -544,16 +544,17 @@ int mxa2a_linear_get_status(mxa2a_linear* l, mxa2a_status* out) {
     if (cudaMemcpy(&st, l->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return MXA2A_ERR_CUDA;
     std::memset(out, 0, sizeof *out);
     out->step = out->segment = out->slot = -1;
-    const unsigned long long launch = st.key >> 8;
-    if ((st.key & 0xFF) != 0 && launch > l->checked_launch) {
-        out->code = (int)(st.key & 0xFF);
-        out->role = st.role;
-        out->block = st.block;
-        out->observed = st.observed;
-        out->expected = st.expected;
-        out->launch = (int64_t)launch;
-    }
-    l->checked_launch = l->launch_id;
+    if ((st.key & 0xFF) == 0) return MXA2A_OK;
+    out->code = (int)(st.key & 0xFF);
+    out->role = st.role;
+    out->block = st.block;
+    out->observed = st.observed;
+    out->expected = st.expected;
+    out->launch = (int64_t)(st.key >> 8);
+    // Read, so cleared on the device (and before the caller's next launch): replays of
+    // a captured run share its launch index, which does not tell whether it was read.
+    if (cudaMemset(&l->status->key, 0, sizeof st.key) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+        return MXA2A_ERR_CUDA;
     return MXA2A_OK;
 }
 

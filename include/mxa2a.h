@@ -684,7 +684,9 @@ int mxa2a_linear_backward(mxa2a_linear *layer, int64_t rows, const void *dy, con
                           const void *counts, void *stream);
 
 /* The device status of a layer's runs (as mxa2a_get_status; role 2 TMA
- * producer, 3 MMA issuer, 4 epilogue, 7 scale copy). */
+ * producer, 3 MMA issuer, 4 epilogue, 7 scale copy).  A status that tells an error
+ * is cleared on the device by this call, so every replay of a captured run
+ * reports its own time-out, under the launch index of the capture. */
 int mxa2a_linear_get_status(mxa2a_linear *layer, mxa2a_status *out);
 
 /* MXA2A_OPT_TIMEOUT_NS (at least 1e6) and MXA2A_OPT_ELEM_TYPES (A is x, B is w), and, for

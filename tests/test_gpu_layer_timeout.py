@@ -64,3 +64,27 @@ def test_time_out_stores_nothing_and_leaves_the_layer_usable(case):
     assert case.layer.status()["code"] == 0
     assert (case.out == 0).all()
     check_layer(layer_inputs([300], 256, 256, 1, dense=True))
+
+
+def test_time_out_of_a_replay_is_reported():
+    case = Case(*SHAPES["pairs"])
+    case.run()                                   # (kernels are loaded before the capture)
+    torch.cuda.synchronize()
+    case.limit(MS)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        case.run()
+    assert case.layer.status()["code"] == 0      # nothing has run yet, and the status has been read
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert timed_out(case.layer.status())    # every replay's own
+        assert case.layer.status()["code"] == 0  # and once
+    # a run of the layer itself between two replays does not hide the second one's
+    case.limit(2000 * MS)
+    case.run()
+    torch.cuda.synchronize()
+    assert case.layer.status()["code"] == 0
+    g.replay()
+    torch.cuda.synchronize()
+    assert timed_out(case.layer.status())
