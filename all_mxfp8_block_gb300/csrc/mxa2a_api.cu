@@ -123,7 +123,7 @@ struct mxa2a_plan {
     CUtensorMap* seg_maps_dev = nullptr;
     CUtensorMap seg_maps_host[kMaxSegments];
     const void* seg_ptrs[kMaxSegments] = {};
-    unsigned long long launch_id = 0, checked_launch = 0;
+    unsigned long long launch_id = 0;
     // ring of (start, end) events around the main GEMM kernel of the last runs
     static constexpr int kEvRing = 4096;
     cudaEvent_t* ev0 = nullptr;
@@ -993,22 +993,25 @@ int mxa2a_get_status(mxa2a_plan* p, mxa2a_status* out) {
     DevStatus st;
     if (cudaMemcpy(&st, p->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return MXA2A_ERR_CUDA;
     std::memset(out, 0, sizeof *out);
-    const unsigned long long launch = st.key >> 8;
     const int code = (int)(st.key & 0xFF);
-    if (code != 0 && launch > p->checked_launch) {
-        out->code = code;
-        out->role = st.role;
-        out->block = st.block;
-        out->step = st.step;
-        out->segment = st.segment;
-        out->slot = st.slot;
-        out->observed = st.observed;
-        out->expected = st.expected;
-        out->launch = (int64_t)launch;
-    } else {
+    if (code == 0) {
         out->step = out->segment = out->slot = -1;
+        return MXA2A_OK;
     }
-    p->checked_launch = p->launch_id;
+    out->code = code;
+    out->role = st.role;
+    out->block = st.block;
+    out->step = st.step;
+    out->segment = st.segment;
+    out->slot = st.slot;
+    out->observed = st.observed;
+    out->expected = st.expected;
+    out->launch = (int64_t)(st.key >> 8);
+    // Read, so cleared on the device (and before the caller's next launch): replays of
+    // a captured run share its launch index, which does not tell whether it was read,
+    // and a replay that finds its index in the status gives up at its first wait.
+    if (cudaMemset(&p->status->key, 0, sizeof st.key) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess)
+        return MXA2A_ERR_CUDA;
     return MXA2A_OK;
 }
 

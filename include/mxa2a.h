@@ -250,9 +250,9 @@ int mxa2a_run_allreduce_unfused(mxa2a_plan *plan, const void *A, const void *A_s
  * split is 1 (MXA2A_INFO_SPLITS, or MXA2A_OPT_SPLIT_K = 1); with a split the
  * call returns MXA2A_ERR_CAPTURE_SPLIT while the stream is capturing, since
  * the partial tiles are tagged with the run's launch index, which a replay
- * does not change.  Replays share that index: a device time-out in one of
- * them stays reported (mxa2a_get_status) for the later ones, and
- * mxa2a_kernel_times does not see replays.
+ * does not change.  Replays share that index: after a device time-out in one
+ * of them the later ones give up at their first wait until mxa2a_get_status
+ * has been called, and mxa2a_kernel_times does not see replays.
  * Errors: MXA2A_ERR_NULL_PTR, MXA2A_ERR_MISALIGNED, MXA2A_ERR_WRONG_DEVICE,
  * MXA2A_ERR_CAPTURE_SPLIT, MXA2A_ERR_CUDA (a launch failed); device
  * time-outs later through mxa2a_get_status.
@@ -321,10 +321,10 @@ int mxa2a_run_host(mxa2a_plan *plan, const void *const *A_seg_host, const void *
 
 /*
  * Copy the device status block to *out (synchronous; call after the runs'
- * stream is synchronised) and mark it read.  out->code is MXA2A_OK unless a
- * launch since the previous call reported a device error.  Returns
- * MXA2A_ERR_NULL_PTR, MXA2A_ERR_WRONG_DEVICE, MXA2A_ERR_CUDA (the copy
- * failed) or MXA2A_OK.
+ * stream is synchronised) and mark it read: an error is cleared on the device.
+ * out->code is MXA2A_OK unless a launch (or a replay of one) since the previous
+ * call reported a device error.  Returns MXA2A_ERR_NULL_PTR,
+ * MXA2A_ERR_WRONG_DEVICE, MXA2A_ERR_CUDA (a copy failed) or MXA2A_OK.
  * Passage: the performance optimisation guide, section 2.1 (deadlocks after
  * moving from barrier_all to wait/notify): a wait that never ends is found by
  * a watchdog time-out followed by a dump of where the signals stopped (a slot
