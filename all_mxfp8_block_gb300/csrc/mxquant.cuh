@@ -194,8 +194,9 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // roundings of its own size (ex2 and reciprocal approximations of 2^-22).
 //   gelu(z) = 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
 // The logistic's argument is kept where e is finite, i.e. z >= -87 (silu) or
-// |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35
-// (silu's slope has no upper limit: e is 0 there).
+// |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35.  The
+// slopes' z is kept at or below 87 (silu) or 10 as well, where they are 1: they
+// multiply z by e, and at +inf that would be inf * 0.
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluA = 2.f * 0.7978845608028654f, kGeluB = 0.044715f;   // 2 sqrt(2 / pi)
@@ -225,7 +226,7 @@ __device__ __forceinline__ float2 act_back2(float2 g, float2 z) {
     if constexpr (kAct == kActRelu) {
         return make_float2(z.x > 0.f ? g.x : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? g.y : (z.y != z.y ? z.y : 0.f));
     } else if constexpr (kAct == kActSilu) {
-        const float2 m = make_float2(max_nan(z.x, -87.f), max_nan(z.y, -87.f)), x = mul2(m, both(-kLog2e));
+        const float2 m = make_float2(min_nan(max_nan(z.x, -87.f), 87.f), min_nan(max_nan(z.y, -87.f), 87.f)), x = mul2(m, both(-kLog2e));
         const float2 e = make_float2(exp2f_approx(x.x), exp2f_approx(x.y)), d = add2(e, both(1.f));
         const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
         return mul2(g, fma2(mul2(m, s), mul2(s, e), s));
