@@ -190,8 +190,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 }
 
 // Activations and their derivatives in fp32 (ids as in the C ABI), through
-// s = logistic(x) = 1 / (1 + e), e = exp(-x), and 1 - s = s e: each to a few
-// roundings of its own size (ex2 and reciprocal approximations of 2^-22).
+// s = logistic(x) = 1 / (1 + e), e = exp(-x), and 1 - s = s e.  Relative errors,
+// in units of 2^-24: e's exponent is rounded before the power is taken, 1.25 |x|
+// (silu, x = z) or 6 |x| (gelu, x = 2 u); ex2, the reciprocal and the products 8
+// more.  So a value is off by 8 near 0 and above it, by some tens where it is far
+// below its argument (at most 83 for silu at -60, 304 for gelu at -8).  A slope's
+// second term has twice that, and its two cancel at the curve's lowest point.
 //   gelu(z) = 0.5 z (1 + tanh u) = z logistic(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
 // The logistic's argument is kept where e is finite, i.e. z >= -87 (silu) or
 // |z| <= 10 (gelu); past it the values are the saturated ones to 1e-35.  The
