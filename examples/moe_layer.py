@@ -49,7 +49,7 @@ class MoELayer:
     def __init__(self, tokens, topk, experts, hidden, ffn, training=False):
         self.tokens, self.k, self.E, self.H, self.F = tokens, topk, experts, hidden, ffn
         self.T = None         # tokens of the forward pass that a backward pass may follow
-        self.rows = rows = max(ALIGN, m.mxa2a_moe_rows(tokens, topk, experts, ALIGN))
+        rows = self.rows_of(tokens)
         i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
         self.offsets, self.counts, self.pos = i32(experts + 1), i32(experts), i32(tokens * topk)
         self.up = m.Linear(experts, rows, ffn, hidden, training)
@@ -68,6 +68,11 @@ class MoELayer:
             self.w1_t, self.w1_ts = codes(experts, hidden, ffn), tiles(hidden, ffn, experts)
             self.w2_t, self.w2_ts = codes(experts, ffn, hidden), tiles(ffn, hidden, experts)
             self.dy, self.dh, self.dxs = bf16(rows, hidden), bf16(rows, ffn), bf16(rows, hidden)
+
+    def rows_of(self, tokens):
+        """Rows that a call with so many tokens works on.  A call passes its own, not the layer's most: the
+        kernels' tiles and splits are chosen by them (a decode step's by a decode step's)."""
+        return max(ALIGN, m.mxa2a_moe_rows(tokens, self.k, self.E, ALIGN))
 
     def load(self, W1, W2, b1=None):
         """W1 fp32 [experts][ffn][hidden], W2 [experts][hidden][ffn], b1 [experts][ffn]: quantised once per update."""
@@ -90,6 +95,7 @@ class MoELayer:
         check("x", x, torch.bfloat16, T, self.H)
         check("expert", expert, torch.int32, T, self.k)
         check("weight", weight, torch.float32, T, self.k)
+        self.rows = self.rows_of(T)
         m.mxa2a_moe_sort(T, self.k, self.E, ALIGN, self.rows, expert, self.offsets, self.counts, self.pos, None)
         return T
 

@@ -645,7 +645,10 @@ mxa2a_linear *mxa2a_linear_create(int groups, int64_t max_rows, int64_t N, int64
  * for every row t of segment g, in one launch.
  *   x [rows][K] codes and x_scale its scale tiles; w [groups][N][K] codes and
  *   w_scale [groups][ceil(K/128)][ceil(N/128)][512] (E4M3 both, or
- *   MXA2A_OPT_ELEM_TYPES); rows <= max_rows.
+ *   MXA2A_OPT_ELEM_TYPES); rows <= max_rows.  The host knows no segment's length:
+ *   tile width, contraction split and grid come from rows, groups, N and K, so a
+ *   call passes the rows that its own tokens may need (mxa2a_moe_rows), not the
+ *   most that its buffers hold.  Every choice is right for every routing.
  *   offsets, counts: the segments of the sort; their alignment must be a
  *   multiple of 32.  NULL (both; groups == 1): all rows.
  *   bias fp32 [groups][N], residual bf16 [rows][N], preact bf16 [rows][N] (the
