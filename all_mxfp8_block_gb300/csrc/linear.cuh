@@ -1,4 +1,4 @@
-// Interface between the linear layer's C ABI (linear_api.cu) and its GEMM
+// Interface between the linear layer's C ABI (operators_api.cu) and its GEMM
 // kernel (linear.cu).
 #pragma once
 #include <cstdint>

@@ -484,7 +484,7 @@ cudaError_t dispatch_mx(const MoeDispatch& a, cudaStream_t stream) {
 template <typename T, int V>
 cudaError_t combine_v(const MoeCombine& a, cudaStream_t stream) {
     constexpr int U = V == 1 ? 4 : 2;
-    if (a.tokens * a.hidden <= 32 * V * 152 * 16) {   // at most 16 warps to an SM in the few-token shape
+    if (a.tokens * a.hidden <= 32ll * V * 16 * a.sms) {   // at most 16 warps to an SM in the few-token shape
         const RowShape r = row_shape(a.hidden, 32 * V);
         return launch(moe_combine_few_kernel<T, V>, dim3((unsigned)(a.tokens * r.parts)), r.threads, 0, 1, stream, a, (int)r.parts);
     }

@@ -1,5 +1,5 @@
 // Launchers of the mixture-of-experts row kernels (moe.cu) and the MX
-// quantiser (mxquant.cu).  All return the cudaError_t of their launch.
+// quantiser (quantize.cu).  All return the cudaError_t of their launch.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -43,6 +43,7 @@ struct MoeCombine {
     const void* residual;    // null: none
     void* out;
     int type;
+    int sms;                 // SMs of the device
 };
 cudaError_t launch_moe_combine(const MoeCombine& a, cudaStream_t stream);
 
@@ -80,6 +81,6 @@ cudaError_t launch_quantize(const Quantize& q, cudaStream_t stream);
 cudaError_t launch_bias_sums(const float* colsum, const Segments& seg, long long cols, float* dbias, cudaStream_t stream);
 // E8M0 bytes [groups][rows][blocks] to scale tiles
 cudaError_t launch_scale_tiles(const uint8_t* s, int groups, long long rows, long long blocks, uint8_t* tiles,
-                               cudaStream_t stream);
+                               int sms, cudaStream_t stream);
 
 }  // namespace mxa2a

@@ -129,7 +129,7 @@ int mxa2a_moe_combine(int64_t tokens, int topk, int64_t hidden, int64_t rows, co
     if (int rc = need_device()) return rc;
     if (!tokens) return MXA2A_OK;
     MoeCombine a = {tokens, hidden, rows, topk, y, static_cast<const int32_t*>(pos), static_cast<const float*>(weight),
-                    residual, out, type};
+                    residual, out, type, device_sms()};
     return cuda_code(launch_moe_combine(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -173,7 +173,7 @@ int mxa2a_scale_tiles(const void* scale, int groups, int64_t rows, int64_t cols,
     if (int rc = need_device()) return rc;
     if (!any) return MXA2A_OK;
     return cuda_code(launch_scale_tiles(static_cast<const uint8_t*>(scale), groups, rows, cols / 32, static_cast<uint8_t*>(tiles),
-                                        static_cast<cudaStream_t>(stream)));
+                                        device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 int mxa2a_quantize(const void* x, int x_type, int64_t ldx, int groups, int64_t rows, int64_t cols, int format, void* codes,

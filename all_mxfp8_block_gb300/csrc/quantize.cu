@@ -253,10 +253,11 @@ cudaError_t launch_bias_sums(const float* colsum, const Segments& seg, long long
     return launch(bias_sums_kernel, grid, 256, 0, 1, stream, colsum, seg, cols, dbias);
 }
 
-cudaError_t launch_scale_tiles(const uint8_t* s, int groups, long long rows, long long blocks, uint8_t* tiles, cudaStream_t stream) {
+cudaError_t launch_scale_tiles(const uint8_t* s, int groups, long long rows, long long blocks, uint8_t* tiles, int sms,
+                               cudaStream_t stream) {
     const int rt = (int)((rows + 127) / 128), bt = (int)((blocks + 3) / 4);
     const long long words = (long long)groups * rt * bt * 128;
-    return launch(scale_tiles_kernel, dim3((unsigned)std::min<long long>((words + 255) / 256, 152 * 16)), 256, 0, 1, stream, s, groups,
+    return launch(scale_tiles_kernel, dim3((unsigned)std::min<long long>((words + 255) / 256, 16ll * sms)), 256, 0, 1, stream, s, groups,
                   rows, blocks, reinterpret_cast<uint32_t*>(tiles), rt, bt);
 }
 
