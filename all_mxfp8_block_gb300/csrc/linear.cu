@@ -28,10 +28,11 @@
 // What bounds it: a few tokens, the weights' bytes and the launch's latency (1
 // token x 7168 x 8192: 15.5 us, 3.9 TB/s; 8 tokens x 4 of 16 experts x 2048 x
 // 7168: 36 us, 6.1 TB/s); wide tiles, the MMAs with the time of a stage around
-// the ring close behind, and over longer runs the power limit (8192^3: 290 us,
-// 3.79 PFLOP/s; the MMAs alone 256 us).  With an expert's weights read for 512
-// rows the loads come from HBM and are the slower side (32 experts x 512 x 2048
-// x 7168: 154 us, 130 us with one weight matrix).
+// the ring close behind, and over longer runs the power limit (8192^3 on normally
+// distributed operands: 310 us, 3.54 PFLOP/s, over seconds 358 us; on codes whose
+// bits switch less 288, of which the MMAs alone are 256).  With an expert's weights
+// read for 512 rows the loads come from HBM and are the slower side (32 experts x
+// 512 x 2048 x 7168: 158 us, 138 us with one weight matrix).
 //
 // Every wait is bounded; after one ran out no role of the CTA starts another tile,
 // a tile given up is not stored (the output is undefined then) and the status
